@@ -18,10 +18,14 @@ from typing import Dict, Optional
 
 import torch
 
+from . import w8 as _w8
+from .w8 import dequant8, gemm8, gemm8_workspace, q8_stride, quant8, rmsnorm8  # noqa: F401
+
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 LIB_PATH = os.path.join(PKG_DIR, "libqamw.so")
 HEADER_PATH = os.path.join(ROOT, "include", "qamw.h")
+W8_HEADER_PATH = os.path.join(ROOT, "include", "qamw_w8.h")
 
 F32, BF16 = 0, 1
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = 0, -1, -2, -3, -4
@@ -83,7 +87,7 @@ def load(path: Optional[str] = None):
                                vp], ctypes.c_int),
         "qamw_status_string": ([ctypes.c_int], ctypes.c_char_p),
     }
-    for name, (args, res) in sig.items():
+    for name, (args, res) in list(sig.items()) + list(_w8.SIGNATURES.items()):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res
@@ -92,9 +96,9 @@ def load(path: Optional[str] = None):
     return lib
 
 
-def header_symbols() -> list:
-    """Names of the functions declared in include/qamw.h."""
-    text = open(HEADER_PATH).read()
+def header_symbols(path: str = HEADER_PATH) -> list:
+    """Names of the functions declared in include/qamw.h (or another header of the library)."""
+    text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(qamw_[a-z0-9_]+)\s*\(", text)))
 

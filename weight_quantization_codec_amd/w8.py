@@ -1,0 +1,245 @@
+"""8-bit integer linear layers (include/qamw_w8.h): rows as int8 codes with a scale each, the norm in
+front of a linear layer with its output in that form, and the product of two matrices in that form.
+
+The binding marshals arguments as the rest of the package does.  Work is queued on the current stream
+of the tensors' device.  Codes are int8 tensors whose rows start on 16-byte boundaries; the functions
+that make codes return rows x d views of buffers with rows of q8_stride(d) bytes.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+SIGNATURES = {
+    "qamw_q8_stride": ([_i32], _sz),
+    "qamw_quant8": ([_vp, ctypes.c_int, _i32, _i32, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp], ctypes.c_int),
+    "qamw_dequant8": ([_vp, _i32, _i32, _i64, _vp, _vp, _vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
+    "qamw_rmsnorm8": ([_vp, ctypes.c_int, _i32, _i32, _i64, _vp, _i64, _vp, ctypes.c_float, _vp, _i64, _vp, _i64, _vp,
+                       _vp, _vp], ctypes.c_int),
+    "qamw_gemm8_workspace": ([_i32, _i32, _i32], _sz),
+    "qamw_gemm8": ([_vp, _i64, _vp, _i32, _vp, _i64, _vp, _i32, _i32, _vp, ctypes.c_int, _i64, _vp, _sz, _vp],
+                   ctypes.c_int),
+}
+
+_INT_MAX = 2**31 - 1
+# limits of include/qamw_w8.h
+W8_MAX_COLS = 32768
+GEMM8_MAX_ROWS = 1 << 24
+GEMM8_MAX_COLS = 131071
+GEMM8_MAX_LD = 1 << 22
+
+
+def _dev(first: torch.Tensor, named) -> torch.device:
+    """The device that every given tensor is on."""
+    dev = first.device
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+    if dev.type != "cuda":
+        raise ValueError("%s must be a device tensor" % named[0][0])
+    return dev
+
+
+def _rows(t, name: str, like: Optional[torch.Tensor] = None) -> int:
+    """A 2-D bf16 or fp32 matrix with contiguous rows, of the size and type of `like`; its row pitch."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("%s must be a 2-D tensor of bfloat16 or float32" % name)
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError("%s must be %s of %s, got %s of %s" % (name, tuple(like.shape), like.dtype, tuple(t.shape), t.dtype))
+    n, d = t.shape
+    if n > _INT_MAX or d > _INT_MAX:
+        raise ValueError("%s is too large: %d x %d" % (name, n, d))
+    s0, s1 = t.stride()
+    if n > 0 and d > 1 and s1 != 1:
+        raise ValueError("%s rows must be contiguous" % name)
+    if n <= 1:
+        return d
+    if s0 < d:
+        raise ValueError("%s rows overlap" % name)
+    return s0
+
+
+def _codes(t, name: str, rows: Optional[int] = None, d: Optional[int] = None) -> int:
+    """A code matrix: rows on 16-byte boundaries, each with the bytes up to the next one in its storage;
+    its row pitch."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype != torch.int8:
+        raise ValueError("%s must be a 2-D tensor of int8" % name)
+    n, k = t.shape
+    if (rows is not None and n != rows) or (d is not None and k != d):
+        raise ValueError("%s must be %s x %s, got %s" % (name, rows, d, tuple(t.shape)))
+    if n > _INT_MAX or k > _INT_MAX:
+        raise ValueError("%s is too large: %d x %d" % (name, n, k))
+    if n == 0 or k == 0:
+        return (k + 15) // 16 * 16
+    s0, s1 = t.stride()
+    if k > 1 and s1 != 1:
+        raise ValueError("%s rows must be contiguous" % name)
+    padded = (k + 15) // 16 * 16
+    ld = s0 if n > 1 else padded
+    if ld % 16 or ld < k or t.data_ptr() % 16:
+        raise ValueError("%s rows must start on 16-byte boundaries and not overlap" % name)
+    if k != padded and t.storage_offset() + (n - 1) * ld + padded > t.untyped_storage().nbytes():
+        raise ValueError("%s ends inside its last row's 16-byte chunk" % name)
+    return ld
+
+
+def _vec(t, name: str, n: int, dtype=torch.float32, optional: bool = False):
+    if t is None:
+        if optional:
+            return
+        raise ValueError("%s is required" % name)
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise ValueError("%s must be a tensor of %s" % (name, dtype))
+    if t.numel() < n:
+        raise ValueError("%s needs at least %d elements, got %d" % (name, n, t.numel()))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dt(t: torch.Tensor) -> int:
+    return 1 if t.dtype == torch.bfloat16 else 0
+
+
+def _call(name: str, dev: torch.device, *args):
+    """Queues a library call on the current stream of `dev`."""
+    from . import _check, load
+    fn = getattr(load(), name)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc:
+        _check(rc, name)
+
+
+def q8_stride(d: int) -> int:
+    """Bytes from one row of codes to the next when rows are packed: d rounded up to 16."""
+    return (d + 15) // 16 * 16 if d > 0 else 0
+
+
+def _empty_codes(rows: int, d: int, dev) -> torch.Tensor:
+    pitch = q8_stride(d)
+    t = torch.empty((rows, pitch), dtype=torch.int8, device=dev)
+    return t if pitch == d else t[:, :d]
+
+
+def quant8(x: torch.Tensor, scale: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, row_scale: Optional[torch.Tensor] = None,
+           status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows of x (rows x d, bf16 or fp32) as (int8 codes, fp32 row scales): of x, of x silu(gate) with a
+    gate, times the channel scale (d fp32) with one.  See qamw_quant8."""
+    ld_x = _rows(x, "x")
+    rows, d = x.shape
+    ld_g = _rows(gate, "gate", like=x) if gate is not None else 0
+    _vec(scale, "scale", d, optional=True)
+    _vec(row_scale, "row_scale", rows, optional=True)
+    _vec(status, "status", 1, torch.int32, optional=True)
+    if out is not None:
+        _codes(out, "out", rows, d)
+    dev = _dev(x, (("x", x), ("gate", gate), ("scale", scale), ("out", out), ("row_scale", row_scale),
+                   ("status", status)))
+    if out is None:
+        out = _empty_codes(rows, d, dev)
+    if row_scale is None:
+        row_scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+    ld_q = _codes(out, "out", rows, d)
+    _call("qamw_quant8", dev, x.data_ptr(), _dt(x), rows, d, ld_x, _ptr(gate), ld_g, _ptr(scale), out.data_ptr(), ld_q,
+          row_scale.data_ptr(), _ptr(status))
+    return out, row_scale
+
+
+def dequant8(codes: torch.Tensor, row_scale: torch.Tensor, scale: Optional[torch.Tensor] = None,
+             out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that codes stand for (rows x d, bf16 or fp32), with the channel scale that quant8
+    multiplied in divided out.  See qamw_dequant8."""
+    ld_q = _codes(codes, "codes")
+    rows, d = codes.shape
+    _vec(row_scale, "row_scale", rows)
+    _vec(scale, "scale", d, optional=True)
+    if out is not None:
+        _rows(out, "out")
+        if tuple(out.shape) != (rows, d):
+            raise ValueError("out must be %d x %d, got %s" % (rows, d, tuple(out.shape)))
+    elif out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    dev = _dev(codes, (("codes", codes), ("row_scale", row_scale), ("scale", scale), ("out", out)))
+    if out is None:
+        out = torch.empty((rows, d), dtype=out_dtype, device=dev)
+    _call("qamw_dequant8", dev, codes.data_ptr(), rows, d, ld_q, row_scale.data_ptr(), _ptr(scale), out.data_ptr(),
+          _dt(out), _rows(out, "out"))
+    return out
+
+
+def rmsnorm8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-5,
+             residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, row_scale: Optional[torch.Tensor] = None,
+             status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Residual addition and root-mean-square norm: (int8 codes of the normalized rows, their fp32 row
+    scales, h = x + residual).  Without a residual h is x itself, and sum_out (if given) a copy of it;
+    sum_out may be x or residual (h in place).  See qamw_rmsnorm8."""
+    ld_x = _rows(x, "x")
+    rows, d = x.shape
+    ld_r = _rows(residual, "residual", like=x) if residual is not None else 0
+    ld_s = _rows(sum_out, "sum_out", like=x) if sum_out is not None else 0
+    _vec(weight, "weight", d, optional=True)
+    _vec(row_scale, "row_scale", rows, optional=True)
+    _vec(status, "status", 1, torch.int32, optional=True)
+    if out is not None:
+        _codes(out, "out", rows, d)
+    dev = _dev(x, (("x", x), ("residual", residual), ("sum_out", sum_out), ("weight", weight), ("out", out),
+                   ("row_scale", row_scale), ("status", status)))
+    if residual is not None and sum_out is None:
+        sum_out = torch.empty((rows, d), dtype=x.dtype, device=dev)
+        ld_s = d
+    if out is None:
+        out = _empty_codes(rows, d, dev)
+    if row_scale is None:
+        row_scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+    ld_q = _codes(out, "out", rows, d)
+    _call("qamw_rmsnorm8", dev, x.data_ptr(), _dt(x), rows, d, ld_x, _ptr(residual), ld_r, _ptr(weight), eps,
+          _ptr(sum_out), ld_s, out.data_ptr(), ld_q, row_scale.data_ptr(), _ptr(status))
+    return out, row_scale, x if sum_out is None else sum_out
+
+
+def gemm8_workspace(M: int, d_out: int, d_in: int) -> int:
+    from . import load
+    return load().qamw_gemm8_workspace(M, d_out, d_in)
+
+
+def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, out_dtype=torch.bfloat16,
+          out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = x w^T of 8-bit activations (M x d_in codes, a scale for each token) and weights (d_out x d_in
+    codes, a scale for each output channel): M x d_out, bf16 or fp32.  See qamw_gemm8."""
+    ld_x, ld_w = _codes(xq, "xq"), _codes(wq, "wq")
+    M, K = xq.shape
+    N = wq.shape[0]
+    if wq.shape[1] != K:
+        raise ValueError("xq has %d columns, wq %d" % (K, wq.shape[1]))
+    _vec(x_scale, "x_scale", M)
+    _vec(w_scale, "w_scale", N)
+    if out is not None:
+        _rows(out, "out")
+        if tuple(out.shape) != (M, N):
+            raise ValueError("out must be %d x %d, got %s" % (M, N, tuple(out.shape)))
+    elif out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    need = gemm8_workspace(M, N, K)
+    _vec(workspace, "workspace", need, torch.uint8, optional=True)
+    dev = _dev(xq, (("xq", xq), ("x_scale", x_scale), ("wq", wq), ("w_scale", w_scale), ("out", out),
+                    ("workspace", workspace)))
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    if workspace is None and need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    _call("qamw_gemm8", dev, xq.data_ptr(), ld_x, x_scale.data_ptr(), M, wq.data_ptr(), ld_w, w_scale.data_ptr(), N, K,
+          out.data_ptr(), _dt(out), _rows(out, "out"), _ptr(workspace), need if workspace is None else workspace.numel())
+    return out
