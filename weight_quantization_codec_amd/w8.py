@@ -32,15 +32,21 @@ GEMM8_MAX_COLS = 131071
 GEMM8_MAX_LD = 1 << 22
 
 
-def _dev(first: torch.Tensor, named) -> torch.device:
-    """The device that every given tensor is on."""
-    dev = first.device
-    for name, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
-    if dev.type != "cuda":
-        raise ValueError("%s must be a device tensor" % named[0][0])
-    return dev
+# The current stream's handle without a Stream object around it: a tenth of the time, in calls that take
+# a few microseconds in all.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _device(names, first, *others) -> int:
+    """The index of the device that all given tensors (None: not given) are on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("%s must be a device tensor" % names.split()[0])
+    for i, t in enumerate(others):
+        if t is not None and t.get_device() != index:
+            raise ValueError("%s is on %s, not on %s" % (names.split()[i + 1], t.device, first.device))
+    return index
 
 
 def _rows(t, name: str, like: Optional[torch.Tensor] = None) -> int:
@@ -86,17 +92,26 @@ def _codes(t, name: str, rows: Optional[int] = None, d: Optional[int] = None) ->
     return ld
 
 
-def _vec(t, name: str, n: int, dtype=torch.float32, optional: bool = False):
-    if t is None:
-        if optional:
-            return
-        raise ValueError("%s is required" % name)
+def _vec(t, name: str, n: int, dtype=torch.float32):
+    """A contiguous vector of at least n elements of dtype."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise ValueError("%s must be a tensor of %s" % (name, dtype))
     if t.numel() < n:
         raise ValueError("%s needs at least %d elements, got %d" % (name, n, t.numel()))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+
+
+def _out(out: Optional[torch.Tensor], dtype, rows: int, d: int) -> int:
+    """The output matrix of a call, given or to be made; its row pitch."""
+    if out is None:
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be bfloat16 or float32")
+        return d
+    ld = _rows(out, "out")
+    if tuple(out.shape) != (rows, d):
+        raise ValueError("out must be %d x %d, got %s" % (rows, d, tuple(out.shape)))
+    return ld
 
 
 def _ptr(t):
@@ -107,17 +122,22 @@ def _dt(t: torch.Tensor) -> int:
     return 1 if t.dtype == torch.bfloat16 else 0
 
 
-def _call(name: str, dev: torch.device, *args):
-    """Queues a library call on the current stream of `dev`."""
-    from . import _check, load
-    fn = getattr(load(), name)
-    index = dev.index
+_fns = {}
+
+
+def _call(name: str, index: int, *args):
+    """Queues a library call on the current stream of device `index`."""
+    fn = _fns.get(name)
+    if fn is None:
+        from . import load
+        fn = _fns[name] = getattr(load(), name)
     if index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        rc = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
     if rc:
+        from . import _check
         _check(rc, name)
 
 
@@ -126,9 +146,9 @@ def q8_stride(d: int) -> int:
     return (d + 15) // 16 * 16 if d > 0 else 0
 
 
-def _empty_codes(rows: int, d: int, dev) -> torch.Tensor:
+def _empty_codes(x: torch.Tensor, rows: int, d: int) -> torch.Tensor:
     pitch = q8_stride(d)
-    t = torch.empty((rows, pitch), dtype=torch.int8, device=dev)
+    t = x.new_empty((rows, pitch), dtype=torch.int8)
     return t if pitch == d else t[:, :d]
 
 
@@ -140,19 +160,19 @@ def quant8(x: torch.Tensor, scale: Optional[torch.Tensor] = None, gate: Optional
     ld_x = _rows(x, "x")
     rows, d = x.shape
     ld_g = _rows(gate, "gate", like=x) if gate is not None else 0
-    _vec(scale, "scale", d, optional=True)
-    _vec(row_scale, "row_scale", rows, optional=True)
-    _vec(status, "status", 1, torch.int32, optional=True)
-    if out is not None:
-        _codes(out, "out", rows, d)
-    dev = _dev(x, (("x", x), ("gate", gate), ("scale", scale), ("out", out), ("row_scale", row_scale),
-                   ("status", status)))
+    if scale is not None:
+        _vec(scale, "scale", d)
+    if row_scale is not None:
+        _vec(row_scale, "row_scale", rows)
+    if status is not None:
+        _vec(status, "status", 1, torch.int32)
+    ld_q = _codes(out, "out", rows, d) if out is not None else q8_stride(d)
+    index = _device("x gate scale out row_scale status", x, gate, scale, out, row_scale, status)
     if out is None:
-        out = _empty_codes(rows, d, dev)
+        out = _empty_codes(x, rows, d)
     if row_scale is None:
-        row_scale = torch.empty((rows,), dtype=torch.float32, device=dev)
-    ld_q = _codes(out, "out", rows, d)
-    _call("qamw_quant8", dev, x.data_ptr(), _dt(x), rows, d, ld_x, _ptr(gate), ld_g, _ptr(scale), out.data_ptr(), ld_q,
+        row_scale = x.new_empty((rows,), dtype=torch.float32)
+    _call("qamw_quant8", index, x.data_ptr(), _dt(x), rows, d, ld_x, _ptr(gate), ld_g, _ptr(scale), out.data_ptr(), ld_q,
           row_scale.data_ptr(), _ptr(status))
     return out, row_scale
 
@@ -164,18 +184,14 @@ def dequant8(codes: torch.Tensor, row_scale: torch.Tensor, scale: Optional[torch
     ld_q = _codes(codes, "codes")
     rows, d = codes.shape
     _vec(row_scale, "row_scale", rows)
-    _vec(scale, "scale", d, optional=True)
-    if out is not None:
-        _rows(out, "out")
-        if tuple(out.shape) != (rows, d):
-            raise ValueError("out must be %d x %d, got %s" % (rows, d, tuple(out.shape)))
-    elif out_dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("out_dtype must be bfloat16 or float32")
-    dev = _dev(codes, (("codes", codes), ("row_scale", row_scale), ("scale", scale), ("out", out)))
+    if scale is not None:
+        _vec(scale, "scale", d)
+    ld_out = _out(out, out_dtype, rows, d)
+    index = _device("codes row_scale scale out", codes, row_scale, scale, out)
     if out is None:
-        out = torch.empty((rows, d), dtype=out_dtype, device=dev)
-    _call("qamw_dequant8", dev, codes.data_ptr(), rows, d, ld_q, row_scale.data_ptr(), _ptr(scale), out.data_ptr(),
-          _dt(out), _rows(out, "out"))
+        out = codes.new_empty((rows, d), dtype=out_dtype)
+    _call("qamw_dequant8", index, codes.data_ptr(), rows, d, ld_q, row_scale.data_ptr(), _ptr(scale), out.data_ptr(),
+          _dt(out), ld_out)
     return out
 
 
@@ -189,30 +205,34 @@ def rmsnorm8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     ld_x = _rows(x, "x")
     rows, d = x.shape
     ld_r = _rows(residual, "residual", like=x) if residual is not None else 0
-    ld_s = _rows(sum_out, "sum_out", like=x) if sum_out is not None else 0
-    _vec(weight, "weight", d, optional=True)
-    _vec(row_scale, "row_scale", rows, optional=True)
-    _vec(status, "status", 1, torch.int32, optional=True)
-    if out is not None:
-        _codes(out, "out", rows, d)
-    dev = _dev(x, (("x", x), ("residual", residual), ("sum_out", sum_out), ("weight", weight), ("out", out),
-                   ("row_scale", row_scale), ("status", status)))
+    ld_s = _rows(sum_out, "sum_out", like=x) if sum_out is not None else d
+    if weight is not None:
+        _vec(weight, "weight", d)
+    if row_scale is not None:
+        _vec(row_scale, "row_scale", rows)
+    if status is not None:
+        _vec(status, "status", 1, torch.int32)
+    ld_q = _codes(out, "out", rows, d) if out is not None else q8_stride(d)
+    index = _device("x residual sum_out weight out row_scale status", x, residual, sum_out, weight, out, row_scale,
+                    status)
     if residual is not None and sum_out is None:
-        sum_out = torch.empty((rows, d), dtype=x.dtype, device=dev)
-        ld_s = d
+        sum_out = x.new_empty((rows, d))
     if out is None:
-        out = _empty_codes(rows, d, dev)
+        out = _empty_codes(x, rows, d)
     if row_scale is None:
-        row_scale = torch.empty((rows,), dtype=torch.float32, device=dev)
-    ld_q = _codes(out, "out", rows, d)
-    _call("qamw_rmsnorm8", dev, x.data_ptr(), _dt(x), rows, d, ld_x, _ptr(residual), ld_r, _ptr(weight), eps,
+        row_scale = x.new_empty((rows,), dtype=torch.float32)
+    _call("qamw_rmsnorm8", index, x.data_ptr(), _dt(x), rows, d, ld_x, _ptr(residual), ld_r, _ptr(weight), eps,
           _ptr(sum_out), ld_s, out.data_ptr(), ld_q, row_scale.data_ptr(), _ptr(status))
     return out, row_scale, x if sum_out is None else sum_out
 
 
 def gemm8_workspace(M: int, d_out: int, d_in: int) -> int:
-    from . import load
-    return load().qamw_gemm8_workspace(M, d_out, d_in)
+    """Bytes of workspace that gemm8 uses (0 for most sizes)."""
+    fn = _fns.get("qamw_gemm8_workspace")
+    if fn is None:
+        from . import load
+        fn = _fns["qamw_gemm8_workspace"] = load().qamw_gemm8_workspace
+    return fn(M, d_out, d_in)
 
 
 def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, out_dtype=torch.bfloat16,
@@ -221,25 +241,20 @@ def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: to
     codes, a scale for each output channel): M x d_out, bf16 or fp32.  See qamw_gemm8."""
     ld_x, ld_w = _codes(xq, "xq"), _codes(wq, "wq")
     M, K = xq.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K:
-        raise ValueError("xq has %d columns, wq %d" % (K, wq.shape[1]))
+    N, wk = wq.shape
+    if wk != K:
+        raise ValueError("xq has %d columns, wq %d" % (K, wk))
     _vec(x_scale, "x_scale", M)
     _vec(w_scale, "w_scale", N)
-    if out is not None:
-        _rows(out, "out")
-        if tuple(out.shape) != (M, N):
-            raise ValueError("out must be %d x %d, got %s" % (M, N, tuple(out.shape)))
-    elif out_dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("out_dtype must be bfloat16 or float32")
+    ld_y = _out(out, out_dtype, M, N)
     need = gemm8_workspace(M, N, K)
-    _vec(workspace, "workspace", need, torch.uint8, optional=True)
-    dev = _dev(xq, (("xq", xq), ("x_scale", x_scale), ("wq", wq), ("w_scale", w_scale), ("out", out),
-                    ("workspace", workspace)))
+    if workspace is not None:
+        _vec(workspace, "workspace", need, torch.uint8)
+    index = _device("xq x_scale wq w_scale out workspace", xq, x_scale, wq, w_scale, out, workspace)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = xq.new_empty((M, N), dtype=out_dtype)
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    _call("qamw_gemm8", dev, xq.data_ptr(), ld_x, x_scale.data_ptr(), M, wq.data_ptr(), ld_w, w_scale.data_ptr(), N, K,
-          out.data_ptr(), _dt(out), _rows(out, "out"), _ptr(workspace), need if workspace is None else workspace.numel())
+        workspace = xq.new_empty((need,), dtype=torch.uint8)
+    _call("qamw_gemm8", index, xq.data_ptr(), ld_x, x_scale.data_ptr(), M, wq.data_ptr(), ld_w, w_scale.data_ptr(), N, K,
+          out.data_ptr(), _dt(out), ld_y, _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out
