@@ -38,15 +38,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _device(names, first, *others) -> int:
-    """The index of the device that all given tensors (None: not given) are on."""
-    index = first.get_device()
+def _not_there(index: int, **tensors):
+    """The error of a call with a tensor that is not on device `index`, the first one's."""
     if index < 0:
-        raise ValueError("%s must be a device tensor" % names.split()[0])
-    for i, t in enumerate(others):
+        raise ValueError("%s must be a device tensor" % next(iter(tensors)))
+    for name, t in tensors.items():
         if t is not None and t.get_device() != index:
-            raise ValueError("%s is on %s, not on %s" % (names.split()[i + 1], t.device, first.device))
-    return index
+            raise ValueError("%s is on %s, not on device %d" % (name, t.device, index))
 
 
 def _rows(t, name: str, like: Optional[torch.Tensor] = None) -> int:
@@ -118,27 +116,28 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _dt(t: torch.Tensor) -> int:
-    return 1 if t.dtype == torch.bfloat16 else 0
+class _Fns(dict):
+    """The library's functions by name, from the first use on."""
 
-
-_fns = {}
-
-
-def _call(name: str, index: int, *args):
-    """Queues a library call on the current stream of device `index`."""
-    fn = _fns.get(name)
-    if fn is None:
+    def __missing__(self, name):
         from . import load
-        fn = _fns[name] = getattr(load(), name)
-    if index == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, _raw_stream(index))
-    if rc:
-        from . import _check
-        _check(rc, name)
+        fn = self[name] = getattr(load(), name)
+        return fn
+
+
+_fns = _Fns()
+_current = torch.cuda.current_device
+
+
+def _elsewhere(fn, index: int, args) -> int:
+    """A call on a device that is not the current one."""
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index))
+
+
+def _failed(rc: int, name: str):
+    from . import _check
+    _check(rc, name)
 
 
 def q8_stride(d: int) -> int:
@@ -146,9 +145,8 @@ def q8_stride(d: int) -> int:
     return (d + 15) // 16 * 16 if d > 0 else 0
 
 
-def _empty_codes(x: torch.Tensor, rows: int, d: int) -> torch.Tensor:
-    pitch = q8_stride(d)
-    t = x.new_empty((rows, pitch), dtype=torch.int8)
+def _empty_codes(x: torch.Tensor, rows: int, d: int, pitch: int) -> torch.Tensor:
+    t = x.new_empty(rows, pitch, dtype=torch.int8)
     return t if pitch == d else t[:, :d]
 
 
@@ -167,13 +165,22 @@ def quant8(x: torch.Tensor, scale: Optional[torch.Tensor] = None, gate: Optional
     if status is not None:
         _vec(status, "status", 1, torch.int32)
     ld_q = _codes(out, "out", rows, d) if out is not None else q8_stride(d)
-    index = _device("x gate scale out row_scale status", x, gate, scale, out, row_scale, status)
+    index = x.get_device()
+    if index < 0 or (gate is not None and gate.get_device() != index) or (
+            scale is not None and scale.get_device() != index) or (out is not None and out.get_device() != index) or (
+            row_scale is not None and row_scale.get_device() != index) or (
+            status is not None and status.get_device() != index):
+        _not_there(index, x=x, gate=gate, scale=scale, out=out, row_scale=row_scale, status=status)
     if out is None:
-        out = _empty_codes(x, rows, d)
+        out = _empty_codes(x, rows, d, ld_q)
     if row_scale is None:
-        row_scale = x.new_empty((rows,), dtype=torch.float32)
-    _call("qamw_quant8", index, x.data_ptr(), _dt(x), rows, d, ld_x, _ptr(gate), ld_g, _ptr(scale), out.data_ptr(), ld_q,
-          row_scale.data_ptr(), _ptr(status))
+        row_scale = x.new_empty(rows, dtype=torch.float32)
+    args = (x.data_ptr(), 1 if x.dtype is torch.bfloat16 else 0, rows, d, ld_x, _ptr(gate), ld_g, _ptr(scale),
+            out.data_ptr(), ld_q, row_scale.data_ptr(), _ptr(status))
+    fn = _fns["qamw_quant8"]
+    rc = fn(*args, _raw_stream(index)) if index == _current() else _elsewhere(fn, index, args)
+    if rc:
+        _failed(rc, "qamw_quant8")
     return out, row_scale
 
 
@@ -187,11 +194,18 @@ def dequant8(codes: torch.Tensor, row_scale: torch.Tensor, scale: Optional[torch
     if scale is not None:
         _vec(scale, "scale", d)
     ld_out = _out(out, out_dtype, rows, d)
-    index = _device("codes row_scale scale out", codes, row_scale, scale, out)
+    index = codes.get_device()
+    if index < 0 or row_scale.get_device() != index or (scale is not None and scale.get_device() != index) or (
+            out is not None and out.get_device() != index):
+        _not_there(index, codes=codes, row_scale=row_scale, scale=scale, out=out)
     if out is None:
         out = codes.new_empty((rows, d), dtype=out_dtype)
-    _call("qamw_dequant8", index, codes.data_ptr(), rows, d, ld_q, row_scale.data_ptr(), _ptr(scale), out.data_ptr(),
-          _dt(out), ld_out)
+    args = (codes.data_ptr(), rows, d, ld_q, row_scale.data_ptr(), _ptr(scale), out.data_ptr(),
+            1 if out.dtype is torch.bfloat16 else 0, ld_out)
+    fn = _fns["qamw_dequant8"]
+    rc = fn(*args, _raw_stream(index)) if index == _current() else _elsewhere(fn, index, args)
+    if rc:
+        _failed(rc, "qamw_dequant8")
     return out
 
 
@@ -213,26 +227,33 @@ def rmsnorm8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     if status is not None:
         _vec(status, "status", 1, torch.int32)
     ld_q = _codes(out, "out", rows, d) if out is not None else q8_stride(d)
-    index = _device("x residual sum_out weight out row_scale status", x, residual, sum_out, weight, out, row_scale,
-                    status)
+    index = x.get_device()
+    if index < 0 or (residual is not None and residual.get_device() != index) or (
+            sum_out is not None and sum_out.get_device() != index) or (
+            weight is not None and weight.get_device() != index) or (
+            out is not None and out.get_device() != index) or (
+            row_scale is not None and row_scale.get_device() != index) or (
+            status is not None and status.get_device() != index):
+        _not_there(index, x=x, residual=residual, sum_out=sum_out, weight=weight, out=out, row_scale=row_scale,
+                   status=status)
     if residual is not None and sum_out is None:
         sum_out = x.new_empty((rows, d))
     if out is None:
-        out = _empty_codes(x, rows, d)
+        out = _empty_codes(x, rows, d, ld_q)
     if row_scale is None:
-        row_scale = x.new_empty((rows,), dtype=torch.float32)
-    _call("qamw_rmsnorm8", index, x.data_ptr(), _dt(x), rows, d, ld_x, _ptr(residual), ld_r, _ptr(weight), eps,
-          _ptr(sum_out), ld_s, out.data_ptr(), ld_q, row_scale.data_ptr(), _ptr(status))
+        row_scale = x.new_empty(rows, dtype=torch.float32)
+    args = (x.data_ptr(), 1 if x.dtype is torch.bfloat16 else 0, rows, d, ld_x, _ptr(residual), ld_r, _ptr(weight), eps,
+            _ptr(sum_out), ld_s, out.data_ptr(), ld_q, row_scale.data_ptr(), _ptr(status))
+    fn = _fns["qamw_rmsnorm8"]
+    rc = fn(*args, _raw_stream(index)) if index == _current() else _elsewhere(fn, index, args)
+    if rc:
+        _failed(rc, "qamw_rmsnorm8")
     return out, row_scale, x if sum_out is None else sum_out
 
 
 def gemm8_workspace(M: int, d_out: int, d_in: int) -> int:
     """Bytes of workspace that gemm8 uses (0 for most sizes)."""
-    fn = _fns.get("qamw_gemm8_workspace")
-    if fn is None:
-        from . import load
-        fn = _fns["qamw_gemm8_workspace"] = load().qamw_gemm8_workspace
-    return fn(M, d_out, d_in)
+    return _fns["qamw_gemm8_workspace"](M, d_out, d_in)
 
 
 def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, out_dtype=torch.bfloat16,
@@ -247,14 +268,22 @@ def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: to
     _vec(x_scale, "x_scale", M)
     _vec(w_scale, "w_scale", N)
     ld_y = _out(out, out_dtype, M, N)
-    need = gemm8_workspace(M, N, K)
+    need = _fns["qamw_gemm8_workspace"](M, N, K)
     if workspace is not None:
         _vec(workspace, "workspace", need, torch.uint8)
-    index = _device("xq x_scale wq w_scale out workspace", xq, x_scale, wq, w_scale, out, workspace)
+    index = xq.get_device()
+    if index < 0 or x_scale.get_device() != index or wq.get_device() != index or w_scale.get_device() != index or (
+            out is not None and out.get_device() != index) or (
+            workspace is not None and workspace.get_device() != index):
+        _not_there(index, xq=xq, x_scale=x_scale, wq=wq, w_scale=w_scale, out=out, workspace=workspace)
     if out is None:
         out = xq.new_empty((M, N), dtype=out_dtype)
     if workspace is None and need:
         workspace = xq.new_empty((need,), dtype=torch.uint8)
-    _call("qamw_gemm8", index, xq.data_ptr(), ld_x, x_scale.data_ptr(), M, wq.data_ptr(), ld_w, w_scale.data_ptr(), N, K,
-          out.data_ptr(), _dt(out), ld_y, _ptr(workspace), 0 if workspace is None else workspace.numel())
+    args = (xq.data_ptr(), ld_x, x_scale.data_ptr(), M, wq.data_ptr(), ld_w, w_scale.data_ptr(), N, K, out.data_ptr(),
+            1 if out.dtype is torch.bfloat16 else 0, ld_y, _ptr(workspace), 0 if workspace is None else workspace.numel())
+    fn = _fns["qamw_gemm8"]
+    rc = fn(*args, _raw_stream(index)) if index == _current() else _elsewhere(fn, index, args)
+    if rc:
+        _failed(rc, "qamw_gemm8")
     return out
