@@ -61,7 +61,7 @@ int qamw_quant8(const void* d_x, qamw_dtype x_dtype, int32_t rows, int32_t d, in
 /* The values that codes stand for:
  *     x^_ij = fl32(q_ij s_i), then times fl32(1 / s_j) in fp32 with d_scale (the d_scale of qamw_quant8),
  * rounded to nearest even for QAMW_BF16.  d_out: rows x d, ld_out >= d, any alignment of rows.
- * 0 <= rows <= QAMW_MAX_ROWS, d >= 1. */
+ * 0 <= rows <= QAMW_MAX_ROWS, 1 <= d <= QAMW_MAX_ROWS (QAMW_ERR_UNSUPPORTED above). */
 int qamw_dequant8(const int8_t* d_q, int32_t rows, int32_t d, int64_t ld_q, const float* d_row_scale,
                   const float* d_scale, void* d_out, qamw_dtype out_dtype, int64_t ld_out, void* stream);
 

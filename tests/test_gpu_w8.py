@@ -190,6 +190,27 @@ def test_rmsnorm8(q, n, d, dtype):
     assert h1 is x
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n,d", [(2000, 4936), (1500, 13000), (900, 5000), (1200, 20480), (4000, 700)])
+def test_rmsnorm8_in_place_many_rows(q, n, d, dtype):
+    """h over x, in rows that several wavefronts share and whose last chunks do not fill them: no wavefront
+    sees what another one has already written."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(n + d)
+    x = torch.randn((n, d), generator=gen, device=DEV)
+    x[:, -8:] *= 10   # the largest values last
+    x = x.to(dtype)
+    r = x.clone()
+    w = torch.rand((d,), generator=gen, device=DEV) + 0.5
+    log("in place %d x %d %s" % (n, d, dtype))
+    c1, s1, h1 = q.rmsnorm8(x, w, residual=r)
+    for over in (0, 1):
+        for _ in range(3):
+            x2, r2 = x.clone(), r.clone()
+            c2, s2, h2 = q.rmsnorm8(x2, w, residual=r2, sum_out=r2 if over else x2)
+            assert torch.equal(s1, s2) and torch.equal(c1, c2) and torch.equal(h1, h2)
+
+
 def test_rmsnorm8_special_rows(q):
     d = 520
     a = np.random.default_rng(6).standard_normal((8, d)).astype(np.float32)
@@ -389,6 +410,46 @@ def test_mlp_block_in_a_graph(q, T):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want_y) and torch.equal(h, want_h), i
+
+
+def test_two_graphs_and_a_shared_workspace(q):
+    """Two products captured into graphs of their own, with a workspace of the caller's that both use, one
+    replayed after the other on one stream."""
+    rng = np.random.default_rng(11)
+    cases = []
+    for M, N, K in ((77, 4096, 11008), (200, 1024, 4096)):
+        assert q.gemm8_workspace(M, N, K) > 0
+        cases.append((_code_matrix(rng, M, K), torch.rand(M, device=DEV), _code_matrix(rng, N, K),
+                      torch.rand(N, device=DEV)))
+    need = max(q.gemm8_workspace(c[0].shape[0], c[2].shape[0], c[0].shape[1]) for c in cases)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    want = [_want(*c, torch.bfloat16) for c in cases]
+    graphs, outs = [], []
+    for c in cases:
+        outs.append(torch.zeros((c[0].shape[0], c[2].shape[0]), dtype=torch.bfloat16, device=DEV))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q.gemm8(*c, out=outs[-1], workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_empty_matrices(q):
+    e = lambda *s, **k: torch.empty(s, device=DEV, **k)
+    c, s = q.quant8(e(0, 64, dtype=torch.bfloat16))
+    assert c.shape == (0, 64) and s.shape == (0,)
+    assert q.dequant8(c, s).shape == (0, 64)
+    c, s, h = q.rmsnorm8(e(0, 64), residual=e(0, 64))
+    assert c.shape == (0, 64) and h.shape == (0, 64)
+    w = torch.zeros((5, 64), dtype=torch.int8, device=DEV)
+    assert q.gemm8(c, s, w, torch.ones(5, device=DEV)).shape == (0, 5)
+    assert q.gemm8(w, torch.ones(5, device=DEV), c, s).shape == (5, 0)
 
 
 def test_two_streams(q):

@@ -79,8 +79,8 @@ def _dequant(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dt=2), ARG), (dict(rows=-1), ARG), (dict(d=0), ARG), (dict(rows=1 << 30), UNSUP), (dict(ld=63), ARG),
-    (dict(codes=None), ARG), (dict(codes=FAKE + 4), ARG), (dict(ld_q=65), ARG), (dict(ld_q=48), ARG), (dict(s=None), ARG),
+    (dict(dt=2), ARG), (dict(rows=-1), ARG), (dict(d=0), ARG), (dict(rows=1 << 30), UNSUP),
+    (dict(d=1 << 30, ld_q=1 << 30, ld=1 << 30), UNSUP), (dict(ld=63), ARG), (dict(codes=None), ARG), (dict(codes=FAKE + 4), ARG), (dict(ld_q=65), ARG), (dict(ld_q=48), ARG), (dict(s=None), ARG),
     (dict(out=None), ARG), (dict(out=FAKE + 1), ARG), (dict(dt=q.F32, out=FAKE + 2), ARG), (dict(scale=FAKE + 1), ARG),
 ])
 def test_dequant8_rejects(lib, kw, code):

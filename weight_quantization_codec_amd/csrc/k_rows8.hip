@@ -249,11 +249,13 @@ __global__ __launch_bounds__(max_waves(V) * kWave) void k_rows8(Rows8Args a, int
             }
             if (KIND != kNorm && row == 0 && bad && a.status) atomicOr(a.status, QAMW_FLAG_BAD_SCALE);
         }
-        if (full > 0) {
+        // (a chunk loaded again does not count: with h in place of x, its thread may have written it already)
 #pragma unroll
-            for (int k = 0; k < V; ++k)
+        for (int k = 0; k < V; ++k) {
+            float m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) top = top_of(top, v[k][i]);
+            for (int i = 0; i < kChunk; ++i) m = top_of(m, v[k][i]);
+            top = t + k * nt < full ? top_of(top, m) : top;
         }
         if (rest && t == 0) {
 #pragma unroll

@@ -64,7 +64,7 @@ int qamw_quant8(const void* d_x, qamw_dtype x_dtype, int32_t rows, int32_t d, in
 int qamw_dequant8(const int8_t* d_q, int32_t rows, int32_t d, int64_t ld_q, const float* d_row_scale,
                   const float* d_scale, void* d_out, qamw_dtype out_dtype, int64_t ld_out, void* stream) {
     if (!is_dtype(out_dtype) || rows < 0 || d < 1 || ld_out < d) return QAMW_ERR_ARG;
-    if (rows > QAMW_MAX_ROWS) return QAMW_ERR_UNSUPPORTED;
+    if (rows > QAMW_MAX_ROWS || d > QAMW_MAX_ROWS) return QAMW_ERR_UNSUPPORTED;
     if (rows == 0) return QAMW_OK;
     if (!codes_ok(d_q, ld_q, d) || !d_row_scale || !d_out || !aligned(d_row_scale, 4) || !aligned(d_scale, 4) ||
         !aligned(d_out, elem_bytes(out_dtype)))
