@@ -25,6 +25,7 @@ SIGNATURES = {
 }
 
 _INT_MAX = 2**31 - 1
+_VALUES = (torch.bfloat16, torch.float32)
 # limits of include/qamw_w8.h
 W8_MAX_COLS = 32768
 GEMM8_MAX_ROWS = 1 << 24
@@ -49,44 +50,47 @@ def _not_there(index: int, **tensors):
 
 def _rows(t, name: str, like: Optional[torch.Tensor] = None) -> int:
     """A 2-D bf16 or fp32 matrix with contiguous rows, of the size and type of `like`; its row pitch."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float32):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _VALUES or t.dim() != 2:
         raise ValueError("%s must be a 2-D tensor of bfloat16 or float32" % name)
     if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
         raise ValueError("%s must be %s of %s, got %s of %s" % (name, tuple(like.shape), like.dtype, tuple(t.shape), t.dtype))
     n, d = t.shape
     if n > _INT_MAX or d > _INT_MAX:
         raise ValueError("%s is too large: %d x %d" % (name, n, d))
-    s0, s1 = t.stride()
-    if n > 0 and d > 1 and s1 != 1:
-        raise ValueError("%s rows must be contiguous" % name)
-    if n <= 1:
+    if t.is_contiguous():
         return d
-    if s0 < d:
+    s0, s1 = t.stride()
+    if d > 1 and s1 != 1:
+        raise ValueError("%s rows must be contiguous" % name)
+    if n > 1 and s0 < d:
         raise ValueError("%s rows overlap" % name)
-    return s0
+    return s0 if n > 1 else d
 
 
 def _codes(t, name: str, rows: Optional[int] = None, d: Optional[int] = None) -> int:
     """A code matrix: rows on 16-byte boundaries, each with the bytes up to the next one in its storage;
     its row pitch."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype != torch.int8:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int8 or t.dim() != 2:
         raise ValueError("%s must be a 2-D tensor of int8" % name)
     n, k = t.shape
     if (rows is not None and n != rows) or (d is not None and k != d):
         raise ValueError("%s must be %s x %s, got %s" % (name, rows, d, tuple(t.shape)))
     if n > _INT_MAX or k > _INT_MAX:
         raise ValueError("%s is too large: %d x %d" % (name, n, k))
-    if n == 0 or k == 0:
-        return (k + 15) // 16 * 16
-    s0, s1 = t.stride()
-    if k > 1 and s1 != 1:
-        raise ValueError("%s rows must be contiguous" % name)
     padded = (k + 15) // 16 * 16
-    ld = s0 if n > 1 else padded
+    if k == padded and t.is_contiguous():
+        ld = k
+    elif n == 0 or k == 0:
+        return padded
+    else:
+        s0, s1 = t.stride()
+        if k > 1 and s1 != 1:
+            raise ValueError("%s rows must be contiguous" % name)
+        ld = s0 if n > 1 else padded
+        if k != padded and t.storage_offset() + (n - 1) * ld + padded > t.untyped_storage().nbytes():
+            raise ValueError("%s ends inside its last row's 16-byte chunk" % name)
     if ld % 16 or ld < k or t.data_ptr() % 16:
         raise ValueError("%s rows must start on 16-byte boundaries and not overlap" % name)
-    if k != padded and t.storage_offset() + (n - 1) * ld + padded > t.untyped_storage().nbytes():
-        raise ValueError("%s ends inside its last row's 16-byte chunk" % name)
     return ld
 
 
@@ -103,7 +107,7 @@ def _vec(t, name: str, n: int, dtype=torch.float32):
 def _out(out: Optional[torch.Tensor], dtype, rows: int, d: int) -> int:
     """The output matrix of a call, given or to be made; its row pitch."""
     if out is None:
-        if dtype not in (torch.bfloat16, torch.float32):
+        if dtype not in _VALUES:
             raise ValueError("out_dtype must be bfloat16 or float32")
         return d
     ld = _rows(out, "out")
@@ -199,7 +203,7 @@ def dequant8(codes: torch.Tensor, row_scale: torch.Tensor, scale: Optional[torch
             out is not None and out.get_device() != index):
         _not_there(index, codes=codes, row_scale=row_scale, scale=scale, out=out)
     if out is None:
-        out = codes.new_empty((rows, d), dtype=out_dtype)
+        out = codes.new_empty(rows, d, dtype=out_dtype)
     args = (codes.data_ptr(), rows, d, ld_q, row_scale.data_ptr(), _ptr(scale), out.data_ptr(),
             1 if out.dtype is torch.bfloat16 else 0, ld_out)
     fn = _fns["qamw_dequant8"]
@@ -237,7 +241,7 @@ def rmsnorm8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
         _not_there(index, x=x, residual=residual, sum_out=sum_out, weight=weight, out=out, row_scale=row_scale,
                    status=status)
     if residual is not None and sum_out is None:
-        sum_out = x.new_empty((rows, d))
+        sum_out = x.new_empty(rows, d)
     if out is None:
         out = _empty_codes(x, rows, d, ld_q)
     if row_scale is None:
@@ -277,9 +281,9 @@ def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: to
             workspace is not None and workspace.get_device() != index):
         _not_there(index, xq=xq, x_scale=x_scale, wq=wq, w_scale=w_scale, out=out, workspace=workspace)
     if out is None:
-        out = xq.new_empty((M, N), dtype=out_dtype)
+        out = xq.new_empty(M, N, dtype=out_dtype)
     if workspace is None and need:
-        workspace = xq.new_empty((need,), dtype=torch.uint8)
+        workspace = xq.new_empty(need, dtype=torch.uint8)
     args = (xq.data_ptr(), ld_x, x_scale.data_ptr(), M, wq.data_ptr(), ld_w, w_scale.data_ptr(), N, K, out.data_ptr(),
             1 if out.dtype is torch.bfloat16 else 0, ld_y, _ptr(workspace), 0 if workspace is None else workspace.numel())
     fn = _fns["qamw_gemm8"]
