@@ -375,7 +375,15 @@ __global__ __launch_bounds__(256) void k_gemm8_join(Gemm8Args a, int splits) {
     if (m >= a.M) return;
     const int* p = reinterpret_cast<const int*>(a.work) + m * pitch + n;
     i32x4 c = *reinterpret_cast<const i32x4*>(p);
-    for (int s = 1; s < splits; ++s) c += *reinterpret_cast<const i32x4*>(p + (int64_t)s * a.M * pitch);
+    int s = 1;
+    for (; s + 3 <= splits; s += 3) {   // three loads under way at a time
+        i32x4 v[3];
+#pragma unroll
+        for (int u = 0; u < 3; ++u) v[u] = *reinterpret_cast<const i32x4*>(p + (int64_t)(s + u) * a.M * pitch);
+#pragma unroll
+        for (int u = 0; u < 3; ++u) c += v[u];
+    }
+    for (; s < splits; ++s) c += *reinterpret_cast<const i32x4*>(p + (int64_t)s * a.M * pitch);
     const float xs = a.xs[m];
     float v[4];
 #pragma unroll
@@ -385,8 +393,11 @@ __global__ __launch_bounds__(256) void k_gemm8_join(Gemm8Args a, int splits) {
         const Out8 o = {{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}};
         if (n + 4 <= a.N)
             *reinterpret_cast<Out8*>(y) = o;
-        else
-            for (int e = 0; n + e < a.N; ++e) y[e] = (uint16_t)(o.w[e / 2] >> (16 * (e % 2)));
+        else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (n + e < a.N) y[e] = (uint16_t)(o.w[e / 2] >> (16 * (e % 2)));
+        }
     } else {
         float* y = reinterpret_cast<float*>(a.y) + m * a.ld_y + n;
 #pragma unroll
@@ -577,48 +588,50 @@ hipError_t launch_thin(const Gemm8Args& a, hipStream_t st) {
 // ------------------------------------------------------------------------------- which kernel
 // Tiles of several sizes, and k split over workgroups where the tiles do not fill the chip.  Larger tiles
 // read less from L2 for each product; smaller ones fill the chip and have shorter starts and ends.  The
-// choice is the least time by a model with constants measured on MI355X (K = 1000 to 13824; M x N from
-// 1 x 1024 to 8192 x 13824; the choice came within 20% of the best of all on 40 sizes, mostly within 5%):
-//   a round of up to 256 tiles takes `start` us and a step (128 bytes of k) `step` us, or as long as L2
-//   takes to deliver the operands of all tiles of the round, at 14 TB/s;
-//   joining the parts of k takes 3 us and the traffic of the sums at 6 TB/s;
-//   the operands come from memory at 4.6 TB/s.
-// The thin kernel (at most 64 activation rows) takes 1.6 us, the weights at 5.9 TB/s and the activations of
-// all its workgroups at 14 TB/s.
+// choice is the least time by a model: rounds of up to 256 workgroups, one a compute unit; a round with
+// a share f of that takes  start + more_start f + steps (step + more_step f^3)  us, for steps of 128 bytes of
+// k; the operands are read from memory once; the sums of k's parts are written and read, behind a launch.
+// The thin kernel (at most 64 activation rows) has the weights once, and the activations once a workgroup.
 struct Plan {
     int tile;     // index into kTiles, or kThin
     int splits;   // parts of k
 };
 struct TileCost {
     int bm, bn;
-    double start, step;
+    double start, more_start, step, more_step;
 };
-constexpr TileCost kTiles[] = {{256, 256, 9.0, 1.2},  {256, 128, 6.0, 0.61}, {128, 128, 5.4, 0.37},
-                               {128, 64, 4.6, 0.29},  {64, 128, 4.6, 0.29},  {64, 64, 4.2, 0.22}};
+// Constants fitted to measurements on MI355X of every tile and 1 to 16 parts on 200 sizes (M from 1 to 8192, N and
+// K from 64 to 13824; weights in cache and not): there the choice takes 1% longer than the best one on
+// average, 20% at most.
+constexpr TileCost kTiles[] = {{256, 256, 8.9, 0.9, 0.89, 0.44}, {256, 128, 5.2, 1.1, 0.54, 0.27},
+                               {128, 128, 3.6, 0.8, 0.37, 0.10}, {128, 64, 2.9, 0.9, 0.27, 0.025},
+                               {64, 128, 2.5, 1.3, 0.35, 0.03},  {64, 64, 2.4, 0.4, 0.21, 0.03}};
+constexpr double kLaunch = 1.3, kMemory = 28e6, kJoin = 2.9, kJoinTraffic = 8.9e6;   // us; bytes a us
+constexpr double kThinStart = 3.9, kThinStep = 0.046, kThinWeights = 10.6e6, kThinActivations = 25.7e6;
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]), kThin = kTileKinds, kThinRows = 64;
 
 Plan plan(int M, int N, int K) {
     Plan best{0, 1};
     double least = 1e300;
-    const double m = M, n = N, k = K, memory = 1.5 + (n * k + m * k) / 4.6e6;
+    const double m = M, n = N, k = K;
     const int64_t steps = (K + 127) / 128;
     if (M <= kThinRows) {
         const int rows = thin_rows(N);
-        const double wgs = (double)((N + rows - 1) / rows), xrows = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
-        least = 1.6 + n * k / 5.9e6 + wgs * xrows * k / 14e6;
+        const double wgs = (double)((N + rows - 1) / rows), x_rows = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+        least = kThinStart + (double)steps * kThinStep + n * k / kThinWeights + wgs * x_rows * k / kThinActivations;
         best.tile = kThin;
     }
     for (int i = 0; i < kTileKinds; ++i) {
         const TileCost& c = kTiles[i];
         const int64_t tiles = (((int64_t)M + c.bm - 1) / c.bm) * (((int64_t)N + c.bn - 1) / c.bn);
-        const double stage = ((m < c.bm ? m : c.bm) + (n < c.bn ? n : c.bn)) * 128;
         for (const int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
             if (s > 1 && (tiles * s > kCus || steps / s < 3)) break;
-            const int64_t rounds = (tiles * s + kCus - 1) / kCus;
-            const double l2 = (double)(tiles * s) / rounds * stage / 14e6;
-            double t = rounds * (c.start + (double)((steps + s - 1) / s) * (c.step > l2 ? c.step : l2));
-            t = t > memory ? t : memory;
-            if (s > 1) t += 3.0 + s * m * n * 8 / 6e6;
+            const int64_t rounds = tiles * s / kCus, rest = tiles * s % kCus;
+            const double part = (double)((steps + s - 1) / s), f = (double)rest / kCus;
+            double t = kLaunch + (double)rounds * (c.start + c.more_start + part * (c.step + c.more_step));
+            if (rest) t += c.start + c.more_start * f + part * (c.step + c.more_step * f * f * f);
+            t += (n * k + m * k) / kMemory;
+            if (s > 1) t += kJoin + s * m * n * 8 / kJoinTraffic;
             if (t < least) {
                 least = t;
                 best = {i, s};

@@ -304,14 +304,16 @@ __global__ __launch_bounds__(max_waves(V) * kWave) void k_rows8(Rows8Args a, int
     }
 }
 
-// How a row is spread: v chunks a thread, w wavefronts.  Many rows fill the chip by themselves: 4, 5 or 8
-// chunks, whichever leaves the fewest lanes idle, so that a compute unit has many bytes under way and few
-// wavefronts wait for each other (13824 x 5120 bf16, 1 chunk a thread 107 us, 2: 67, 4: 58, 5: 54).  Few rows
-// are spread over more wavefronts (515 x 4100 fp32: 2 chunks 6.0 us, 8: 7.0).
+// How a row is spread: v chunks a thread, w wavefronts.  Many rows fill the chip by themselves: of bf16 4, 5
+// or 8 chunks, whichever leaves the fewest lanes idle, so that a compute unit has many bytes under way and few
+// wavefronts wait for each other (13824 x 5120 bf16, 1 chunk a thread 107 us, 2: 67, 4: 58, 5: 54); of fp32,
+// twice the bytes, 4 (8 chunks of fp32 do not fit the registers of 8 wavefronts, and a kernel with scratch
+// memory takes 12 us longer to start: for the widest rows only).  Few rows are spread over more wavefronts
+// (515 x 4100 fp32: 2 chunks 6.0 us, 8: 7.0).
 struct RowShape {
     int v, w;
 };
-RowShape row_shape(int rows, int d) {
+RowShape row_shape(int rows, int d, bool bf) {
     const int full = d / kChunk, waves = full < kWave ? 1 : (full + kWave - 1) / kWave;
     RowShape best{0, 0};
     auto consider = [&](int v) {
@@ -320,7 +322,8 @@ RowShape row_shape(int rows, int d) {
     };
     if (waves == 1) consider(1);
     else if (rows < 1024) consider(2);
-    else consider(4), consider(5), consider(8);
+    if (best.v == 0) consider(4);
+    if (best.v == 4 && bf) consider(5), consider(8);
     if (best.v == 0) consider(8);   // up to 32768 columns
     return best;
 }
@@ -342,12 +345,14 @@ hipError_t launch_rows_v(const Rows8Args& a, int w, hipStream_t st) {
 
 template <int KIND, bool BF, bool FACTOR>
 hipError_t launch_rows_f(const Rows8Args& a, hipStream_t st) {
-    const RowShape s = row_shape(a.rows, a.d);
+    const RowShape s = row_shape(a.rows, a.d, BF);
     switch (s.v) {
     case 1: return launch_rows_v<KIND, BF, FACTOR, 1>(a, s.w, st);
     case 2: return launch_rows_v<KIND, BF, FACTOR, 2>(a, s.w, st);
     case 4: return launch_rows_v<KIND, BF, FACTOR, 4>(a, s.w, st);
-    case 5: return launch_rows_v<KIND, BF, FACTOR, 5>(a, s.w, st);
+    case 5:
+        if constexpr (BF) return launch_rows_v<KIND, BF, FACTOR, 5>(a, s.w, st);
+        [[fallthrough]];
     default: return launch_rows_v<KIND, BF, FACTOR, 8>(a, s.w, st);
     }
 }
