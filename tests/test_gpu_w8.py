@@ -452,6 +452,80 @@ def test_empty_matrices(q):
     assert q.gemm8(w, torch.ones(5, device=DEV), c, s).shape == (5, 0)
 
 
+def _host_calls(q, rng):
+    """Ordinary calls, and the same for the compiled module."""
+    h = q.w8._host
+    T = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(DEV)
+    x, wide, w = T(37, 1003), T(9, 640).bfloat16(), T(1003).abs() + 0.1
+    c, s = q.quant8(T(37, 1003))
+    big = torch.zeros((40, 1024), dtype=torch.int8, device=DEV)
+    cw, sw = _code_matrix(rng, 50, 1003, 16), T(50).abs()
+    return [
+        (lambda: q.quant8(x), lambda: h.quant8(x, None, None)),
+        (lambda: q.quant8(x, scale=w), lambda: h.quant8(x, w, None)),
+        (lambda: q.quant8(wide[:, 320:], gate=wide[:, :320]), lambda: h.quant8(wide[:, 320:], None, wide[:, :320])),
+        (lambda: q.dequant8(c, s), lambda: h.dequant8(c, s, None, True)),
+        (lambda: q.dequant8(c, s, scale=w, out_dtype=torch.float32), lambda: h.dequant8(c, s, w, False)),
+        (lambda: q.dequant8(big[:37, 16:1019], s), lambda: h.dequant8(big[:37, 16:1019], s, None, True)),
+        (lambda: q.rmsnorm8(x, w, eps=1e-3), lambda: h.rmsnorm8(x, w, 1e-3, None)),
+        (lambda: q.rmsnorm8(x, residual=x), lambda: h.rmsnorm8(x, None, 1e-5, x)),
+        (lambda: q.gemm8(c, s, cw, sw), lambda: h.gemm8(c, s, cw, sw, True)),
+        (lambda: q.gemm8(c, s, cw, sw, out_dtype=torch.float32), lambda: h.gemm8(c, s, cw, sw, False)),
+    ]
+
+
+def test_both_ways_through_the_binding(q, monkeypatch):
+    """The compiled module takes the ordinary calls, and gives what the long way through w8.py gives."""
+    flat = lambda r: [t.clone() for t in (r if isinstance(r, tuple) else (r,))]
+    for call, direct in _host_calls(q, np.random.default_rng(13)):
+        short, made = flat(call()), direct()
+        assert made is not None
+        made = flat(made)
+        with monkeypatch.context() as m:
+            m.setattr(q.w8, "_host", None)
+            long = flat(call())
+        for a, b, c in zip(short, long, made):
+            assert a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride()
+            assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_calls_keep_no_memory(q):
+    calls = [c for c, _ in _host_calls(q, np.random.default_rng(14))]
+    for c in calls:
+        c()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for _ in range(50):
+        for c in calls:
+            c()
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before
+
+
+def test_unusual_calls_are_left_to_the_long_way(q):
+    h = q.w8._host
+    f = lambda *s, **k: torch.zeros(s, device=DEV, **k)
+    i8 = torch.int8
+    for r in (h.quant8(f(4, 8).half(), None, None), h.quant8(f(4, 8).t(), None, None), h.quant8(f(8), None, None),
+              h.quant8(f(0, 8), None, None), h.quant8(f(4, 8).cpu(), None, None), h.quant8(f(4, 8), f(7), None),
+              h.quant8(f(4, 8), None, f(4, 7)), h.quant8(f(4, 8), None, f(4, 8).bfloat16()), h.quant8(3, None, None),
+              h.quant8(f(4, 8)), h.quant8(f(2, 40000), None, None),
+              h.dequant8(f(4, 8), f(4), None, True), h.dequant8(f(4, 24, dtype=i8)[:, :8], f(4), None, True),
+              h.dequant8(f(4, 16, dtype=i8), f(3), None, True), h.dequant8(f(4, 16, dtype=i8), f(4).double(), None, True),
+              h.rmsnorm8(f(4, 8), f(8), -1.0, None), h.rmsnorm8(f(4, 8), f(8), "a", None),
+              h.rmsnorm8(f(4, 8), None, 1e-5, f(3, 8)), h.rmsnorm8(f(4, 8), None, 1e-5, f(4, 8).cpu()),
+              h.gemm8(f(4, 16, dtype=i8), f(4), f(5, 32, dtype=i8), f(5), True),
+              h.gemm8(f(4, 16, dtype=i8), f(4), f(5, 16, dtype=i8), f(4), True),
+              h.gemm8(f(4, 16, dtype=i8), f(4), f(5, 16, dtype=i8), f(10)[::2], True)):
+        assert r is None
+    with pytest.raises(q.QamwError):
+        q.quant8(f(2, 40000))
+    with pytest.raises(q.QamwError):
+        q.rmsnorm8(f(4, 8), eps=-1.0)
+    with pytest.raises(ValueError, match="on cpu"):
+        q.rmsnorm8(f(4, 8), residual=f(4, 8).cpu())
+
+
 def test_two_streams(q):
     """Calls on two streams at once, each with its own buffers, give what they give alone."""
     cases = [_mlp_case(q, T, 512, 1000, seed=T) for T in (40, 200)]

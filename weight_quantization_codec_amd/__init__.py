@@ -93,6 +93,7 @@ def load(path: Optional[str] = None):
         fn.restype = res
     if path is None:
         _lib = lib
+        _w8.bind(lib)
     return lib
 
 

@@ -11,6 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqamw.so")
+HOST = os.path.join(PKG, "_w8_host.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "qamw")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -51,5 +52,27 @@ def build(jobs: int = 8) -> str:
     return LIB
 
 
+def build_host() -> str:
+    """Compile the binding's host module (csrc/w8_host.cpp) against the installed torch."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    tmp = HOST + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
+    for d in cpp_extension.include_paths("cuda"):
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "w8_host.cpp"), "-o", tmp]
+    for d in cpp_extension.library_paths():
+        cmd += ["-L", d]
+    cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for w8_host.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr[-4000:]))
+    os.replace(tmp, HOST)
+    return HOST
+
+
 if __name__ == "__main__":
     print(build())
+    print(build_host())

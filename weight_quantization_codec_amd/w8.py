@@ -1,7 +1,9 @@
 """8-bit integer linear layers (include/qamw_w8.h): rows as int8 codes with a scale each, the norm in
 front of a linear layer with its output in that form, and the product of two matrices in that form.
 
-The binding marshals arguments as the rest of the package does.  Work is queued on the current stream
+The binding marshals arguments as the rest of the package does; ordinary calls (matrices on the current
+device, outputs made here) take a short way through the compiled module _w8_host, with the same checks,
+and every other call, all errors among them, the way through this file.  Work is queued on the current stream
 of the tensors' device.  Codes are int8 tensors whose rows start on 16-byte boundaries; the functions
 that make codes return rows x d views of buffers with rows of q8_stride(d) bytes.
 """
@@ -11,6 +13,11 @@ import ctypes
 from typing import Optional, Tuple
 
 import torch
+
+try:
+    from . import _w8_host as _host
+except ImportError:   # not built: every call takes the long way
+    _host = None
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 SIGNATURES = {
@@ -120,6 +127,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def bind(lib):
+    """Gives the compiled module the functions of the loaded library."""
+    if _host is not None:
+        names = ("qamw_quant8", "qamw_dequant8", "qamw_rmsnorm8", "qamw_gemm8_workspace", "qamw_gemm8")
+        _host.bind(*[ctypes.cast(getattr(lib, n), _vp).value for n in names])
+
+
 class _Fns(dict):
     """The library's functions by name, from the first use on."""
 
@@ -159,6 +173,10 @@ def quant8(x: torch.Tensor, scale: Optional[torch.Tensor] = None, gate: Optional
            status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Rows of x (rows x d, bf16 or fp32) as (int8 codes, fp32 row scales): of x, of x silu(gate) with a
     gate, times the channel scale (d fp32) with one.  See qamw_quant8."""
+    if out is None and row_scale is None and status is None and _host is not None:
+        made = _host.quant8(x, scale, gate)
+        if made is not None:
+            return made
     ld_x = _rows(x, "x")
     rows, d = x.shape
     ld_g = _rows(gate, "gate", like=x) if gate is not None else 0
@@ -192,6 +210,10 @@ def dequant8(codes: torch.Tensor, row_scale: torch.Tensor, scale: Optional[torch
              out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values that codes stand for (rows x d, bf16 or fp32), with the channel scale that quant8
     multiplied in divided out.  See qamw_dequant8."""
+    if out is None and out_dtype in _VALUES and _host is not None:
+        out = _host.dequant8(codes, row_scale, scale, out_dtype is torch.bfloat16)
+        if out is not None:
+            return out
     ld_q = _codes(codes, "codes")
     rows, d = codes.shape
     _vec(row_scale, "row_scale", rows)
@@ -220,6 +242,10 @@ def rmsnorm8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     """Residual addition and root-mean-square norm: (int8 codes of the normalized rows, their fp32 row
     scales, h = x + residual).  Without a residual h is x itself, and sum_out (if given) a copy of it;
     sum_out may be x or residual (h in place).  See qamw_rmsnorm8."""
+    if sum_out is None and out is None and row_scale is None and status is None and _host is not None:
+        made = _host.rmsnorm8(x, weight, eps, residual)
+        if made is not None:
+            return made
     ld_x = _rows(x, "x")
     rows, d = x.shape
     ld_r = _rows(residual, "residual", like=x) if residual is not None else 0
@@ -264,6 +290,10 @@ def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: to
           out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y = x w^T of 8-bit activations (M x d_in codes, a scale for each token) and weights (d_out x d_in
     codes, a scale for each output channel): M x d_out, bf16 or fp32.  See qamw_gemm8."""
+    if out is None and workspace is None and out_dtype in _VALUES and _host is not None:
+        out = _host.gemm8(xq, x_scale, wq, w_scale, out_dtype is torch.bfloat16)
+        if out is not None:
+            return out
     ld_x, ld_w = _codes(xq, "xq"), _codes(wq, "wq")
     M, K = xq.shape
     N, wk = wq.shape
