@@ -93,10 +93,12 @@ int qamw_rmsnorm8(const void* d_x, qamw_dtype x_dtype, int32_t rows, int32_t d, 
  *   d_ws, ws_bytes      at least qamw_gemm8_workspace(M, d_out, d_in) bytes, 256-byte aligned (may be
  *                       NULL where that is 0); nothing in it has to start at zero.
  * 0 <= M, d_out <= QAMW_GEMM8_MAX_ROWS, 1 <= d_in <= QAMW_GEMM8_MAX_COLS (32-bit sums are exact up to
- * there), ld_x and ld_w <= QAMW_GEMM8_MAX_LD (QAMW_ERR_UNSUPPORTED above).  M = 0 or d_out = 0 is a no-op. */
+ * there), M * d_out <= QAMW_GEMM8_MAX_OUT, ld_x and ld_w <= QAMW_GEMM8_MAX_LD (QAMW_ERR_UNSUPPORTED above).
+ * M = 0 or d_out = 0 is a no-op. */
 #define QAMW_GEMM8_MAX_ROWS (1 << 24)
 #define QAMW_GEMM8_MAX_COLS 131071
 #define QAMW_GEMM8_MAX_LD (1 << 22)
+#define QAMW_GEMM8_MAX_OUT (1ll << 38)
 size_t qamw_gemm8_workspace(int32_t M, int32_t d_out, int32_t d_in);
 int qamw_gemm8(const int8_t* d_xq, int64_t ld_x, const float* d_xs, int32_t M, const int8_t* d_wq, int64_t ld_w,
                const float* d_wscale, int32_t d_out, int32_t d_in, void* d_y, qamw_dtype y_dtype, int64_t ld_y,

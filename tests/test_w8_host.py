@@ -49,9 +49,9 @@ def test_stride(lib):
 
 def test_header_limits_match_binding():
     text = open(q.W8_HEADER_PATH).read()
-    for name in ("W8_MAX_COLS", "GEMM8_MAX_ROWS", "GEMM8_MAX_COLS", "GEMM8_MAX_LD"):
+    for name in ("W8_MAX_COLS", "GEMM8_MAX_ROWS", "GEMM8_MAX_COLS", "GEMM8_MAX_LD", "GEMM8_MAX_OUT"):
         m = re.search(r"#define QAMW_%s (.*)" % name, text)
-        assert m and eval(m.group(1)) == getattr(q.w8, name), name
+        assert m and eval(m.group(1).replace("ll", "")) == getattr(q.w8, name), name
 
 
 def _quant(lib, **kw):
@@ -132,7 +132,7 @@ def test_gemm8_rejects(lib, kw, code):
 
 def test_gemm8_workspace(lib):
     """Workspace sizes are bounded, 0 for sizes that are refused, and a short one is refused."""
-    for bad in ((-1, 4, 4), (4, -1, 4), (4, 4, 0), (4, 4, 131072), ((1 << 24) + 1, 4, 4)):
+    for bad in ((-1, 4, 4), (4, -1, 4), (4, 4, 0), (4, 4, 131072), ((1 << 24) + 1, 4, 4), (1 << 20, 1 << 19, 64)):
         assert lib.qamw_gemm8_workspace(*bad) == 0
     for M in (1, 16, 17, 33, 64, 77, 128, 200, 256, 300, 512, 1500, 8192):
         for N, K in ((64, 13824), (4096, 11008), (5120, 5120), (13824, 5120)):

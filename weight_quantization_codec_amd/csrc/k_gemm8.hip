@@ -321,13 +321,13 @@ __global__ __launch_bounds__(256, 1) void k_gemm8(Gemm8Args a, int tiles_m, int 
                 const int byte = (n * 32 + 8 * g + 4 * h) * kEs;
                 uint8_t* p = mine + r * kRow + (((byte / 16) ^ r) % kChunks) * 16 + byte % 16;
                 if constexpr (OUT == kSums) {
-                    *reinterpret_cast<int4*>(p) = make_int4(acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2],
-                                                            acc[n][m][4 * g + 3]);
+                    *reinterpret_cast<i32x4*>(p) = i32x4{acc[n][m][4 * g], acc[n][m][4 * g + 1],
+                                                         acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
                     continue;
                 }
-                const float v[4] = {(float)acc[n][m][4 * g] * xs * ws[n][g].x, (float)acc[n][m][4 * g + 1] * xs * ws[n][g].y,
-                                    (float)acc[n][m][4 * g + 2] * xs * ws[n][g].z,
-                                    (float)acc[n][m][4 * g + 3] * xs * ws[n][g].w};
+                const float4 w = ws[n][g];
+                const float v[4] = {(float)acc[n][m][4 * g] * xs * w.x, (float)acc[n][m][4 * g + 1] * xs * w.y,
+                                    (float)acc[n][m][4 * g + 2] * xs * w.z, (float)acc[n][m][4 * g + 3] * xs * w.w};
                 if constexpr (OUT == kBf16)
                     *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
                 else
@@ -427,8 +427,8 @@ hipError_t launch_tile_kernel(const Gemm8Args& a, int tiles_m, int tiles_n, int 
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_big_lds(kernel, C::kLds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n * splits)), dim3(256), C::kLds, st, a, tiles_m, tiles_n,
-                       splits);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n * splits)), dim3(256), C::kLds, st, a, tiles_m,
+                       tiles_n, splits);
     return hipGetLastError();
 }
 
@@ -445,20 +445,8 @@ hipError_t launch_tiles(const Gemm8Args& a, int splits, hipStream_t st) {
             hipLaunchKernelGGL((k_gemm8_join<false>), grid, dim3(256), 0, st, a, splits);
         return hipGetLastError();
     }
-    const int64_t slab = (1 << 22) / tiles_n;   // row tiles a launch: the grid stays below 2^32 work items
-    for (int64_t m = 0; m < tiles_m; m += slab) {
-        Gemm8Args s = a;
-        const int64_t tiles = tiles_m - m < slab ? tiles_m - m : slab, rows = (int64_t)a.M - m * BM;
-        s.xq += m * BM * a.ld_x;
-        s.xs += m * BM;
-        s.M = (int)(rows < tiles * BM ? rows : tiles * BM);
-        s.y = reinterpret_cast<char*>(a.y) + m * BM * a.ld_y * (a.y_bf16 ? 2 : 4);
-        const hipError_t e =
-            a.y_bf16 ? launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kBf16>(s, (int)tiles, (int)tiles_n, 1, st)
-                     : launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kF32>(s, (int)tiles, (int)tiles_n, 1, st);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kBf16>(a, (int)tiles_m, (int)tiles_n, 1, st)
+                    : launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kF32>(a, (int)tiles_m, (int)tiles_n, 1, st);
 }
 
 // Weight rows of a workgroup: at most 32, and the same for all workgroups of all rounds over the compute
@@ -493,7 +481,8 @@ __global__ __launch_bounds__(W * kWave) void k_gemm8_thin(Gemm8Args a, int rows)
     const uint32_t size_x = (uint32_t)(a.M - 1) * (uint32_t)a.ld_x + pad_k;
     auto load = [&](int u, int slot) {   // past the wavefront's part: from empty buffers
         const uint32_t at = (uint32_t)u * 128;
-        const u32x4 rw = rsrc_of(base_w + at, u < u1 ? size_w - at : 0), rx = rsrc_of(base_x + at, u < u1 ? size_x - at : 0);
+        const u32x4 rw = rsrc_of(base_w + at, u < u1 ? size_w - at : 0);
+        const u32x4 rx = rsrc_of(base_x + at, u < u1 ? size_x - at : 0);
         asm volatile("s_nop 4" ::"s"(rw), "s"(rx));
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) load_lds16(i < 4 ? rw : rx, voff[i], ring + slot * kUnit + i * 1024);
@@ -608,6 +597,7 @@ constexpr TileCost kTiles[] = {{256, 256, 8.9, 0.9, 0.89, 0.44}, {256, 128, 5.2,
                                {64, 128, 2.5, 1.3, 0.35, 0.03},  {64, 64, 2.4, 0.4, 0.21, 0.03}};
 constexpr double kLaunch = 1.3, kMemory = 28e6, kJoin = 2.9, kJoinTraffic = 8.9e6;   // us; bytes a us
 constexpr double kThinStart = 3.9, kThinStep = 0.046, kThinWeights = 10.6e6, kThinActivations = 25.7e6;
+constexpr int64_t kMaxTiles = 1 << 23;   // grids of 256 threads a tile stay below 2^32
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]), kThin = kTileKinds, kThinRows = 64;
 
 Plan plan(int M, int N, int K) {
@@ -624,6 +614,7 @@ Plan plan(int M, int N, int K) {
     for (int i = 0; i < kTileKinds; ++i) {
         const TileCost& c = kTiles[i];
         const int64_t tiles = (((int64_t)M + c.bm - 1) / c.bm) * (((int64_t)N + c.bn - 1) / c.bn);
+        if (tiles > kMaxTiles) continue;   // of 256 x 256 tiles there are never more
         for (const int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
             if (s > 1 && (tiles * s > kCus || steps / s < 3)) break;
             const int64_t rounds = tiles * s / kCus, rest = tiles * s % kCus;

@@ -9,6 +9,12 @@ using namespace qamw;
 
 namespace {
 
+// sizes of the product that the kernels take
+bool gemm8_fits(int32_t M, int32_t d_out, int32_t d_in) {
+    return M <= QAMW_GEMM8_MAX_ROWS && d_out <= QAMW_GEMM8_MAX_ROWS && d_in <= QAMW_GEMM8_MAX_COLS &&
+           (int64_t)M * d_out <= QAMW_GEMM8_MAX_OUT;
+}
+
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 int hip_rc(hipError_t e) { return e == hipSuccess ? QAMW_OK : QAMW_ERR_HIP; }
@@ -117,9 +123,7 @@ int qamw_rmsnorm8(const void* d_x, qamw_dtype x_dtype, int32_t rows, int32_t d, 
 }
 
 size_t qamw_gemm8_workspace(int32_t M, int32_t d_out, int32_t d_in) {
-    if (M < 0 || d_out < 0 || d_in < 1 || M > QAMW_GEMM8_MAX_ROWS || d_out > QAMW_GEMM8_MAX_ROWS ||
-        d_in > QAMW_GEMM8_MAX_COLS)
-        return 0;
+    if (M < 0 || d_out < 0 || d_in < 1 || !gemm8_fits(M, d_out, d_in)) return 0;
     return gemm8_workspace(M, d_out, d_in);
 }
 
@@ -127,8 +131,7 @@ int qamw_gemm8(const int8_t* d_xq, int64_t ld_x, const float* d_xs, int32_t M, c
                const float* d_wscale, int32_t d_out, int32_t d_in, void* d_y, qamw_dtype y_dtype, int64_t ld_y,
                void* d_ws, size_t ws_bytes, void* stream) {
     if (!is_dtype(y_dtype) || M < 0 || d_out < 0 || d_in < 1 || ld_y < d_out) return QAMW_ERR_ARG;
-    if (M > QAMW_GEMM8_MAX_ROWS || d_out > QAMW_GEMM8_MAX_ROWS || d_in > QAMW_GEMM8_MAX_COLS ||
-        ld_x > QAMW_GEMM8_MAX_LD || ld_w > QAMW_GEMM8_MAX_LD)
+    if (!gemm8_fits(M, d_out, d_in) || ld_x > QAMW_GEMM8_MAX_LD || ld_w > QAMW_GEMM8_MAX_LD)
         return QAMW_ERR_UNSUPPORTED;
     if (M == 0 || d_out == 0) return QAMW_OK;
     if (!codes_ok(d_xq, ld_x, d_in) || !codes_ok(d_wq, ld_w, d_in) || !d_xs || !d_wscale || !d_y ||

@@ -38,6 +38,7 @@ W8_MAX_COLS = 32768
 GEMM8_MAX_ROWS = 1 << 24
 GEMM8_MAX_COLS = 131071
 GEMM8_MAX_LD = 1 << 22
+GEMM8_MAX_OUT = 1 << 38
 
 
 # The current stream's handle without a Stream object around it: a tenth of the time, in calls that take
@@ -60,7 +61,8 @@ def _rows(t, name: str, like: Optional[torch.Tensor] = None) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype not in _VALUES or t.dim() != 2:
         raise ValueError("%s must be a 2-D tensor of bfloat16 or float32" % name)
     if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError("%s must be %s of %s, got %s of %s" % (name, tuple(like.shape), like.dtype, tuple(t.shape), t.dtype))
+        raise ValueError("%s must be %s of %s, got %s of %s"
+                         % (name, tuple(like.shape), like.dtype, tuple(t.shape), t.dtype))
     n, d = t.shape
     if n > _INT_MAX or d > _INT_MAX:
         raise ValueError("%s is too large: %d x %d" % (name, n, d))
@@ -315,7 +317,8 @@ def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: to
     if workspace is None and need:
         workspace = xq.new_empty(need, dtype=torch.uint8)
     args = (xq.data_ptr(), ld_x, x_scale.data_ptr(), M, wq.data_ptr(), ld_w, w_scale.data_ptr(), N, K, out.data_ptr(),
-            1 if out.dtype is torch.bfloat16 else 0, ld_y, _ptr(workspace), 0 if workspace is None else workspace.numel())
+            1 if out.dtype is torch.bfloat16 else 0, ld_y, _ptr(workspace),
+            0 if workspace is None else workspace.numel())
     fn = _fns["qamw_gemm8"]
     rc = fn(*args, _raw_stream(index)) if index == _current() else _elsewhere(fn, index, args)
     if rc:
