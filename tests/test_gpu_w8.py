@@ -211,6 +211,43 @@ def test_rmsnorm8_in_place_many_rows(q, n, d, dtype):
             assert torch.equal(s1, s2) and torch.equal(c1, c2) and torch.equal(h1, h2)
 
 
+# enough rows for the kernels that hold 2 to 8 chunks a thread, each with lanes that have none at their last chunk
+MANY = [(6000, 520), (1500, 2056), (800, 4001), (620, 5120), (400, 8192), (230, 13824), (180, 17000), (150, 20480),
+        (95, 32768)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n,d", MANY)
+def test_many_rows(q, n, d, dtype):
+    rng = np.random.default_rng(n + d)
+    x, xf = _rows(_values(rng, n, d), dtype, 0, 0)
+    r, rf = _rows(_values(rng, n, d), dtype, 1, 1)
+    w = np.exp(0.3 * rng.standard_normal(d)).astype(np.float32)
+    wd = torch.from_numpy(w).to(DEV)
+    log("many rows %d x %d %s" % (n, d, dtype))
+    for sc, st in ((None, None), (w, wd)):
+        want, ws = ref.quant8(xf, sc)
+        buf = _code_buffer(n, d)
+        _, s = q.quant8(x, scale=st, out=buf[:n, :d])
+        _check_codes(buf, n, d, want)
+        _same(s, ws)
+        want, s64, h = ref.rmsnorm8(xf, sc, 1e-5, rf)
+        buf = _code_buffer(n, d)
+        _, s, hs = q.rmsnorm8(x, st, residual=r, out=buf[:n, :d])
+        _check_codes(buf, n, d, want)
+        s = s.cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(s - s64) <= s64 * (2.0 ** -24 + 2.0 ** -36))
+        _same(hs.float(), ref.to_bf16(h) if dtype == torch.bfloat16 else h)
+    # gated: silu(0) = 0 exactly, and silu(100) = 100 in fp32: codes and scales of the rows 100 x, where the gate
+    # is 100, and zeros elsewhere
+    gate = torch.full((n, d), 100.0, device=DEV)
+    gate[::3] = 0
+    c, s = q.quant8(x, gate=gate.to(dtype))
+    want, ws = ref.quant8(np.where(np.arange(n)[:, None] % 3 == 0, np.float32(0), xf * np.float32(100)))
+    assert np.array_equal(c.cpu().numpy(), want)
+    _same(s, ws)
+
+
 def test_rmsnorm8_special_rows(q):
     d = 520
     a = np.random.default_rng(6).standard_normal((8, d)).astype(np.float32)

@@ -308,8 +308,9 @@ __global__ __launch_bounds__(max_waves(V) * kWave) void k_rows8(Rows8Args a, int
 // or 8 chunks, whichever leaves the fewest lanes idle, so that a compute unit has many bytes under way and few
 // wavefronts wait for each other (13824 x 5120 bf16, 1 chunk a thread 107 us, 2: 67, 4: 58, 5: 54); of fp32,
 // twice the bytes, 4 (8 chunks of fp32 do not fit the registers of 8 wavefronts, and a kernel with scratch
-// memory takes 12 us longer to start: for the widest rows only).  Few rows are spread over more wavefronts
-// (515 x 4100 fp32: 2 chunks 6.0 us, 8: 7.0).
+// memory takes 12 us longer to start: for the widest rows only).  Less work is spread over more wavefronts: 2
+// chunks below 3 million values (512 x 4096 norm bf16: 2 chunks 6.1 us, 4: 6.8; 1000 x 6336: 15.3 and 12.7), 1 for
+// up to 256 rows (256 x 2048: 3.8 us, 2: 4.1).
 struct RowShape {
     int v, w;
 };
@@ -320,8 +321,8 @@ RowShape row_shape(int rows, int d, bool bf) {
         const int w = (waves + v - 1) / v;
         if (w <= max_waves(v) && (best.v == 0 || v * w < best.v * best.w)) best = {v, w};
     };
-    if (waves == 1) consider(1);
-    else if (rows < 1024) consider(2);
+    if (waves == 1 || (rows <= 256 && waves <= 10)) consider(1);
+    else if (waves == 2 || (int64_t)rows * d < 3000000) consider(2);
     if (best.v == 0) consider(4);
     if (best.v == 4 && bf) consider(5), consider(8);
     if (best.v == 0) consider(8);   // up to 32768 columns
