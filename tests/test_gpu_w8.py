@@ -332,6 +332,21 @@ def test_gemm8_large(q, M, N, K):
         _check_product(q, M, N, K, od)
 
 
+# Sizes at which each kind of tile is chosen, with k whole and in parts, most with a ragged end of k, and the
+# kernel for few rows at each of its widths.
+@pytest.mark.parametrize("M,N,K", [
+    (1233, 7060, 756), (786, 9426, 17),                                       # 256 x 256
+    (1275, 4960, 440), (273, 11373, 18), (200, 5833, 12948), (1502, 1393, 12032),     # 256 x 128
+    (896, 4143, 346), (133, 11089, 17), (431, 1691, 11717), (87, 2768, 11524),        # 128 x 128
+    (2336, 607, 820), (3285, 269, 21), (679, 350, 11734), (2401, 16, 11536),          # 128 x 64
+    (433, 2830, 62), (200, 4153, 18), (47, 6050, 11362), (17, 13930, 13109),          # 64 x 128
+    (131, 757, 53), (405, 85, 4879), (1, 19, 11132), (127, 213, 6194),                # 64 x 64
+    (8, 5120, 1001), (9, 4568, 6656), (32, 13824, 640), (33, 1365, 2049), (63, 4102, 4090)])   # few rows
+def test_gemm8_every_kernel(q, M, N, K):
+    for od in (torch.bfloat16, torch.float32):
+        _check_product(q, M, N, K, od, extra=16 * (M % 2), pad=N % 2)
+
+
 def test_gemm8_deepest(q):
     """K at its limit, every product at its largest: sums of 131071 * 2^14 < 2^31."""
     K = q.w8.GEMM8_MAX_COLS

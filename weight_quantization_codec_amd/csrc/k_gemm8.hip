@@ -433,20 +433,25 @@ hipError_t launch_tile_kernel(const Gemm8Args& a, int tiles_m, int tiles_n, int 
 }
 
 template <int BM, int BN, int WM, int KS, int S, int SP, int FA>
-hipError_t launch_tiles(const Gemm8Args& a, int splits, hipStream_t st) {
-    const int64_t tiles_m = ((int64_t)a.M + BM - 1) / BM, tiles_n = ((int64_t)a.N + BN - 1) / BN;
-    if (splits > 1) {
-        hipError_t e = launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kSums>(a, (int)tiles_m, (int)tiles_n, splits, st);
-        if (e != hipSuccess) return e;
-        const dim3 grid((unsigned)(((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256));
-        if (a.y_bf16)
-            hipLaunchKernelGGL((k_gemm8_join<true>), grid, dim3(256), 0, st, a, splits);
-        else
-            hipLaunchKernelGGL((k_gemm8_join<false>), grid, dim3(256), 0, st, a, splits);
-        return hipGetLastError();
-    }
-    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kBf16>(a, (int)tiles_m, (int)tiles_n, 1, st)
-                    : launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kF32>(a, (int)tiles_m, (int)tiles_n, 1, st);
+hipError_t launch_tiles(const Gemm8Args& a, hipStream_t st) {
+    const int tiles_m = (int)(((int64_t)a.M + BM - 1) / BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
+    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kBf16>(a, tiles_m, tiles_n, 1, st)
+                    : launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kF32>(a, tiles_m, tiles_n, 1, st);
+}
+
+// The same, or with k in parts and their join.
+template <int BM, int BN, int WM, int KS, int S, int SP, int FA>
+hipError_t launch_tiles_or_parts(const Gemm8Args& a, int splits, hipStream_t st) {
+    if (splits == 1) return launch_tiles<BM, BN, WM, KS, S, SP, FA>(a, st);
+    const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
+    const hipError_t e = launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kSums>(a, tiles_m, tiles_n, splits, st);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)(((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256));
+    if (a.y_bf16)
+        hipLaunchKernelGGL((k_gemm8_join<true>), grid, dim3(256), 0, st, a, splits);
+    else
+        hipLaunchKernelGGL((k_gemm8_join<false>), grid, dim3(256), 0, st, a, splits);
+    return hipGetLastError();
 }
 
 // Weight rows of a workgroup: at most 32, and the same for all workgroups of all rounds over the compute
@@ -616,7 +621,7 @@ Plan plan(int M, int N, int K) {
         const int64_t tiles = (((int64_t)M + c.bm - 1) / c.bm) * (((int64_t)N + c.bn - 1) / c.bn);
         if (tiles > kMaxTiles) continue;   // of 256 x 256 tiles there are never more
         for (const int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            if (s > 1 && (tiles * s > kCus || steps / s < 3)) break;
+            if (s > 1 && (i == 0 || tiles * s > kCus || steps / s < 3)) break;   // the largest tiles gain nothing by it
             const int64_t rounds = tiles * s / kCus, rest = tiles * s % kCus;
             const double part = (double)((steps + s - 1) / s), f = (double)rest / kCus;
             double t = kLaunch + (double)rounds * (c.start + c.more_start + part * (c.step + c.more_step));
@@ -643,12 +648,12 @@ size_t gemm8_workspace(int M, int N, int K) {
 hipError_t launch_gemm8(const Gemm8Args& a, hipStream_t st) {
     const Plan p = plan(a.M, a.N, a.K);
     switch (p.tile) {
-    case 0: return launch_tiles<256, 256, 2, 128, 2, 48, 0>(a, p.splits, st);
-    case 1: return launch_tiles<256, 128, 2, 128, 3, 32, 0>(a, p.splits, st);
-    case 2: return launch_tiles<128, 128, 2, 128, 4, 16, 0>(a, p.splits, st);
-    case 3: return launch_tiles<128, 64, 4, 128, 6, 8, 0>(a, p.splits, st);
-    case 4: return launch_tiles<64, 128, 2, 128, 6, 8, 0>(a, p.splits, st);
-    case 5: return launch_tiles<64, 64, 2, 128, 8, 4, 0>(a, p.splits, st);
+    case 0: return launch_tiles<256, 256, 2, 128, 2, 48, 0>(a, st);
+    case 1: return launch_tiles_or_parts<256, 128, 2, 128, 3, 32, 0>(a, p.splits, st);
+    case 2: return launch_tiles_or_parts<128, 128, 2, 128, 4, 16, 0>(a, p.splits, st);
+    case 3: return launch_tiles_or_parts<128, 64, 4, 128, 6, 8, 0>(a, p.splits, st);
+    case 4: return launch_tiles_or_parts<64, 128, 2, 128, 6, 8, 0>(a, p.splits, st);
+    case 5: return launch_tiles_or_parts<64, 64, 2, 128, 8, 4, 0>(a, p.splits, st);
     default: return a.y_bf16 ? launch_thin<kBf16>(a, st) : launch_thin<kF32>(a, st);
     }
 }
