@@ -91,7 +91,8 @@ int qamw_rmsnorm8(const void* d_x, qamw_dtype x_dtype, int32_t rows, int32_t d, 
  *   d_wq, ld_w, d_wscale   d_out x d_in codes and d_out fp32 channel scales.
  *   d_y, y_dtype, ld_y  M x d_out, ld_y >= d_out; it overlaps no input.
  *   d_ws, ws_bytes      at least qamw_gemm8_workspace(M, d_out, d_in) bytes, 256-byte aligned (may be
- *                       NULL where that is 0); nothing in it has to start at zero.
+ *                       NULL where that is 0); nothing in it has to start at zero.  Calls that may
+ *                       overlap (on two streams, in two captured graphs) need one each.
  * 0 <= M, d_out <= QAMW_GEMM8_MAX_ROWS, 1 <= d_in <= QAMW_GEMM8_MAX_COLS (32-bit sums are exact up to
  * there), M * d_out <= QAMW_GEMM8_MAX_OUT, ld_x and ld_w <= QAMW_GEMM8_MAX_LD (QAMW_ERR_UNSUPPORTED above).
  * M = 0 or d_out = 0 is a no-op. */

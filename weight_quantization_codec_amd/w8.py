@@ -291,7 +291,8 @@ def gemm8_workspace(M: int, d_out: int, d_in: int) -> int:
 def gemm8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, out_dtype=torch.bfloat16,
           out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y = x w^T of 8-bit activations (M x d_in codes, a scale for each token) and weights (d_out x d_in
-    codes, a scale for each output channel): M x d_out, bf16 or fp32.  See qamw_gemm8."""
+    codes, a scale for each output channel): M x d_out, bf16 or fp32.  Calls that may overlap need a
+    workspace each, or none given.  See qamw_gemm8."""
     if out is None and workspace is None and out_dtype in _VALUES and _host is not None:
         out = _host.gemm8(xq, x_scale, wq, w_scale, out_dtype is torch.bfloat16)
         if out is not None:
