@@ -1,0 +1,57 @@
+"""The compiled short way of the 8-bit binding: what it does with failures, with the interpreter lock, and
+with products that need a workspace."""
+import ctypes
+
+import pytest
+import torch
+
+from helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+def _bind(q, fn):
+    """The compiled module with `fn` in place of every function of the library that launches."""
+    address = ctypes.cast(fn, ctypes.c_void_p).value
+    size = ctypes.cast(q.load().qamw_gemm8_workspace, ctypes.c_void_p).value
+    q.w8._host.bind(address, address, address, size, address, q.w8._failed)
+
+
+def _tensors():
+    return torch.ones((4, 64), device=DEV), torch.ones((4, 64), dtype=torch.int8, device=DEV), torch.ones(4, device=DEV)
+
+
+def _calls(q):
+    x, c, s = _tensors()
+    return [lambda: q.quant8(x), lambda: q.dequant8(c, s), lambda: q.rmsnorm8(x, residual=x), lambda: q.gemm8(c, s, c, s)]
+
+
+@pytest.mark.parametrize("which", range(4), ids=["quant8", "dequant8", "rmsnorm8", "gemm8"])
+def test_a_failed_launch_is_an_error(q, which):
+    """An error of the runtime, which may come behind a kernel that is already queued, is raised: the call is not
+    queued a second time."""
+    call, seen = _calls(q)[which], []
+    fake = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: seen.append(1) or q.ERR_HIP)
+    try:
+        _bind(q, fake)
+        with pytest.raises(q.QamwError) as e:
+            call()
+        assert e.value.code == q.ERR_HIP and len(seen) == 1
+    finally:
+        q.w8.bind(q.load())
+    call()
+
+
+def test_memory_that_is_not_there_is_asked_for_once(q):
+    """Without room for the output the allocator's error comes out as it is, and the call ends there."""
+    c = torch.ones((1 << 16, 16), dtype=torch.int8, device=DEV)
+    s = torch.ones(1 << 16, device=DEV)
+    ooms = lambda: torch.cuda.memory_stats()["num_ooms"]
+    before = ooms()
+    torch.cuda.set_per_process_memory_fraction(0.02)   # of 288 GB; the output takes 17
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            q.gemm8(c, s, c, s, out_dtype=torch.float32)
+        assert ooms() == before + 1
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)

@@ -1,7 +1,8 @@
 // The ordinary calls of the 8-bit operators, without the interpreter between their checks: matrices and
 // vectors as they mostly are, on the current device, with outputs made here.  Every other call (given
 // outputs, wrong arguments, other devices, empty matrices) is left to the checks of w8.py: a function here
-// returns None for it, before anything is queued.
+// returns None for it, before anything is queued.  What fails behind the checks (no memory for an output, an
+// error of the runtime, which may come with a kernel already queued) is raised here, as w8.py raises it.
 //
 // A call on few rows is over sooner on the GPU (2 to 7 us) than the interpreter has checked its arguments, made
 // its outputs and passed it on: quant8 7.5 us there and 5.5 here, dequant8 6.6 and 4.6, rmsnorm8 with a residual
@@ -12,6 +13,7 @@
 #include <ATen/ATen.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "qamw_w8.h"
@@ -28,7 +30,19 @@ struct Entry {
     decltype(&qamw_gemm8) gemm8;
 } lib;
 
-struct Skip {};   // not an ordinary call
+struct Skip {};     // not an ordinary call
+struct Raised {};   // a Python error is set
+
+PyObject* failed = nullptr;   // failed(return code, function) raises
+
+// The answer of the library: done, or a refusal, before anything was queued (w8.py gives its reason), or an
+// error of the runtime.
+void check(int rc, const char* name) {
+    if (rc == QAMW_OK) return;
+    if (rc == QAMW_ERR_ARG || rc == QAMW_ERR_UNSUPPORTED || rc == QAMW_ERR_WORKSPACE) throw Skip{};
+    Py_XDECREF(PyObject_CallFunction(failed, "is", rc, name));
+    throw Raised{};
+}
 
 const Tensor& tensor(PyObject* o) {
     if (!THPVariable_CheckExact(o)) throw Skip{};
@@ -36,7 +50,7 @@ const Tensor& tensor(PyObject* o) {
 }
 
 void on(const Tensor& t, int device) {
-    if (!t.is_cuda() || t.get_device() != device) throw Skip{};
+    if (!t.is_cuda() || t.get_device() != device || t.layout() != at::kStrided) throw Skip{};
 }
 
 struct Rows {
@@ -96,23 +110,32 @@ Tensor make_codes(const Tensor& like, int64_t n, int64_t d) {
 
 int64_t pitch_of(int64_t d) { return (d + 15) / 16 * 16; }
 
-// A tuple of new references.
+// A tuple of new references; null if one of them is.
 PyObject* tuple(std::initializer_list<PyObject*> items) {
     PyObject* t = PyTuple_New((Py_ssize_t)items.size());
+    bool whole = t;
     Py_ssize_t i = 0;
-    for (PyObject* o : items) PyTuple_SET_ITEM(t, i++, o);
+    for (PyObject* o : items) {
+        whole = whole && o;
+        if (t) PyTuple_SET_ITEM(t, i++, o);
+        else Py_XDECREF(o);
+    }
+    if (!whole) Py_CLEAR(t);
     return t;
 }
 
 template <typename F>
 PyObject* ordinary(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
+    HANDLE_TH_ERRORS
     try {
         if (given != wanted || !lib.gemm8) throw Skip{};
         return f();
-    } catch (...) {
-        PyErr_Clear();
+    } catch (const Skip&) {
         Py_RETURN_NONE;
+    } catch (const Raised&) {
+        return nullptr;
     }
+    END_HANDLE_TH_ERRORS
 }
 
 PyObject* quant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -124,9 +147,9 @@ PyObject* quant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Rows g{nullptr, 0, 0, 0};
         if (a[2] != Py_None) g = rows(tensor(a[2]), dev, &x);
         Tensor q = make_codes(x, r.n, r.d), s = make(x, {r.n}, at::kFloat);
-        if (lib.quant8(r.p, dtype(x), r.n, r.d, r.ld, g.p, g.ld, scale, q.data_ptr<int8_t>(), pitch_of(r.d),
-                       s.data_ptr<float>(), nullptr, stream(dev)))
-            throw Skip{};
+        check(lib.quant8(r.p, dtype(x), r.n, r.d, r.ld, g.p, g.ld, scale, q.data_ptr<int8_t>(), pitch_of(r.d),
+                         s.data_ptr<float>(), nullptr, stream(dev)),
+              "qamw_quant8");
         return tuple({THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(s))});
     });
 }
@@ -139,8 +162,8 @@ PyObject* dequant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float* s = vec(tensor(a[1]), dev, r.n);
         const float* scale = a[2] == Py_None ? nullptr : vec(tensor(a[2]), dev, r.d);
         Tensor y = make(c, {r.n, r.d}, a[3] == Py_True ? at::kBFloat16 : at::kFloat);
-        if (lib.dequant8((const int8_t*)r.p, r.n, r.d, r.ld, s, scale, y.data_ptr(), dtype(y), r.d, stream(dev)))
-            throw Skip{};
+        check(lib.dequant8((const int8_t*)r.p, r.n, r.d, r.ld, s, scale, y.data_ptr(), dtype(y), r.d, stream(dev)),
+              "qamw_dequant8");
         return THPVariable_Wrap(std::move(y));
     });
 }
@@ -152,7 +175,10 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rows r = rows(x, dev);
         const float* w = a[1] == Py_None ? nullptr : vec(tensor(a[1]), dev, r.d);
         const double eps = PyFloat_AsDouble(a[2]);
-        if (PyErr_Occurred()) throw Skip{};
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            throw Skip{};
+        }
         Rows o{nullptr, 0, 0, 0};
         Tensor h;
         if (a[3] != Py_None) {
@@ -160,9 +186,9 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
             h = make(x, {r.n, r.d}, x.scalar_type());
         }
         Tensor q = make_codes(x, r.n, r.d), s = make(x, {r.n}, at::kFloat);
-        if (lib.rmsnorm8(r.p, dtype(x), r.n, r.d, r.ld, o.p, o.ld, w, (float)eps, h.defined() ? h.data_ptr() : nullptr,
-                         r.d, q.data_ptr<int8_t>(), pitch_of(r.d), s.data_ptr<float>(), nullptr, stream(dev)))
-            throw Skip{};
+        check(lib.rmsnorm8(r.p, dtype(x), r.n, r.d, r.ld, o.p, o.ld, w, (float)eps, h.defined() ? h.data_ptr() : nullptr,
+                           r.d, q.data_ptr<int8_t>(), pitch_of(r.d), s.data_ptr<float>(), nullptr, stream(dev)),
+              "qamw_rmsnorm8");
         PyObject* sum = h.defined() ? THPVariable_Wrap(std::move(h)) : Py_NewRef(a[0]);   // without a residual: x
         return tuple({THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(s)), sum});
     });
@@ -179,20 +205,27 @@ PyObject* gemm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensor y = make(xq, {x.n, w.n}, a[4] == Py_True ? at::kBFloat16 : at::kFloat), work;
         const size_t need = lib.gemm8_workspace(x.n, w.n, x.d);
         if (need) work = make(xq, {(int64_t)need}, at::kByte);
-        if (lib.gemm8((const int8_t*)x.p, x.ld, xs, x.n, (const int8_t*)w.p, w.ld, ws, w.n, x.d, y.data_ptr(), dtype(y),
-                      w.n, need ? work.data_ptr() : nullptr, need, stream(dev)))
-            throw Skip{};
+        check(lib.gemm8((const int8_t*)x.p, x.ld, xs, x.n, (const int8_t*)w.p, w.ld, ws, w.n, x.d, y.data_ptr(), dtype(y),
+                        w.n, need ? work.data_ptr() : nullptr, need, stream(dev)),
+              "qamw_gemm8");
         return THPVariable_Wrap(std::move(y));
     });
 }
 
-// bind(quant8, dequant8, rmsnorm8, gemm8_workspace, gemm8): the library's functions, as addresses.
+// bind(quant8, dequant8, rmsnorm8, gemm8_workspace, gemm8, failed): the library's functions, as addresses, and
+// what raises the error of a return code.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* p[5] = {};
-    for (Py_ssize_t i = 0; i < 5 && i < n; ++i) {
+    if (n != 6) {
+        PyErr_SetString(PyExc_TypeError, "bind takes 5 addresses and a callable");
+        return nullptr;
+    }
+    void* p[5];
+    for (Py_ssize_t i = 0; i < 5; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred()) return nullptr;
     }
+    Py_INCREF(a[5]);
+    Py_XSETREF(failed, a[5]);
     lib = {(decltype(lib.quant8))p[0], (decltype(lib.dequant8))p[1], (decltype(lib.rmsnorm8))p[2],
            (decltype(lib.gemm8_workspace))p[3], (decltype(lib.gemm8))p[4]};
     Py_RETURN_NONE;

@@ -133,7 +133,7 @@ def bind(lib):
     """Gives the compiled module the functions of the loaded library."""
     if _host is not None:
         names = ("qamw_quant8", "qamw_dequant8", "qamw_rmsnorm8", "qamw_gemm8_workspace", "qamw_gemm8")
-        _host.bind(*[ctypes.cast(getattr(lib, n), _vp).value for n in names])
+        _host.bind(*[ctypes.cast(getattr(lib, n), _vp).value for n in names], _failed)
 
 
 class _Fns(dict):
