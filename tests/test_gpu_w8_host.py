@@ -55,3 +55,18 @@ def test_memory_that_is_not_there_is_asked_for_once(q):
         assert ooms() == before + 1
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
+
+
+def test_other_threads_run_during_a_launch(q):
+    """The library is called without the interpreter lock, as through ctypes: in place of the library's functions
+    stands the interpreter's own check for the lock, which gives 0 (no error) only where it is not held."""
+    h, (x, c, s) = q.w8._host, _tensors()
+    assert ctypes.pythonapi.PyGILState_Check() == 1   # held here
+    try:
+        _bind(q, ctypes.pythonapi.PyGILState_Check)
+        assert h.quant8(x, None, None) is not None
+        assert h.dequant8(c, s, None, True) is not None
+        assert h.rmsnorm8(x, None, 1e-5, x) is not None
+        assert h.gemm8(c, s, c, s, True) is not None
+    finally:
+        q.w8.bind(q.load())

@@ -4,6 +4,9 @@
 // returns None for it, before anything is queued.  What fails behind the checks (no memory for an output, an
 // error of the runtime, which may come with a kernel already queued) is raised here, as w8.py raises it.
 //
+// The interpreter's lock is released while outputs are allocated and the library is called, which may wait (for
+// memory, for room in a queue): other threads run meanwhile.
+//
 // A call on few rows is over sooner on the GPU (2 to 7 us) than the interpreter has checked its arguments, made
 // its outputs and passed it on: quant8 7.5 us there and 5.5 here, dequant8 6.6 and 4.6, rmsnorm8 with a residual
 // 10 and 6.5, gemm8 8.4 and 4.4, of which the launch is 3.5.
@@ -124,6 +127,14 @@ PyObject* tuple(std::initializer_list<PyObject*> items) {
     return t;
 }
 
+// The interpreter's lock is free as long as one of these lives.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 template <typename F>
 PyObject* ordinary(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
     HANDLE_TH_ERRORS
@@ -146,10 +157,16 @@ PyObject* quant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float* scale = a[1] == Py_None ? nullptr : vec(tensor(a[1]), dev, r.d);
         Rows g{nullptr, 0, 0, 0};
         if (a[2] != Py_None) g = rows(tensor(a[2]), dev, &x);
-        Tensor q = make_codes(x, r.n, r.d), s = make(x, {r.n}, at::kFloat);
-        check(lib.quant8(r.p, dtype(x), r.n, r.d, r.ld, g.p, g.ld, scale, q.data_ptr<int8_t>(), pitch_of(r.d),
-                         s.data_ptr<float>(), nullptr, stream(dev)),
-              "qamw_quant8");
+        Tensor q, s;
+        int rc;
+        {
+            const Unlocked unlocked;
+            q = make_codes(x, r.n, r.d);
+            s = make(x, {r.n}, at::kFloat);
+            rc = lib.quant8(r.p, dtype(x), r.n, r.d, r.ld, g.p, g.ld, scale, q.data_ptr<int8_t>(), pitch_of(r.d),
+                            s.data_ptr<float>(), nullptr, stream(dev));
+        }
+        check(rc, "qamw_quant8");
         return tuple({THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(s))});
     });
 }
@@ -161,9 +178,14 @@ PyObject* dequant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rows r = codes(c, dev);
         const float* s = vec(tensor(a[1]), dev, r.n);
         const float* scale = a[2] == Py_None ? nullptr : vec(tensor(a[2]), dev, r.d);
-        Tensor y = make(c, {r.n, r.d}, a[3] == Py_True ? at::kBFloat16 : at::kFloat);
-        check(lib.dequant8((const int8_t*)r.p, r.n, r.d, r.ld, s, scale, y.data_ptr(), dtype(y), r.d, stream(dev)),
-              "qamw_dequant8");
+        Tensor y;
+        int rc;
+        {
+            const Unlocked unlocked;
+            y = make(c, {r.n, r.d}, a[3] == Py_True ? at::kBFloat16 : at::kFloat);
+            rc = lib.dequant8((const int8_t*)r.p, r.n, r.d, r.ld, s, scale, y.data_ptr(), dtype(y), r.d, stream(dev));
+        }
+        check(rc, "qamw_dequant8");
         return THPVariable_Wrap(std::move(y));
     });
 }
@@ -180,15 +202,18 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
             throw Skip{};
         }
         Rows o{nullptr, 0, 0, 0};
-        Tensor h;
-        if (a[3] != Py_None) {
-            o = rows(tensor(a[3]), dev, &x);
-            h = make(x, {r.n, r.d}, x.scalar_type());
+        if (a[3] != Py_None) o = rows(tensor(a[3]), dev, &x);
+        Tensor h, q, s;
+        int rc;
+        {
+            const Unlocked unlocked;
+            if (o.p) h = make(x, {r.n, r.d}, x.scalar_type());
+            q = make_codes(x, r.n, r.d);
+            s = make(x, {r.n}, at::kFloat);
+            rc = lib.rmsnorm8(r.p, dtype(x), r.n, r.d, r.ld, o.p, o.ld, w, (float)eps, o.p ? h.data_ptr() : nullptr, r.d,
+                              q.data_ptr<int8_t>(), pitch_of(r.d), s.data_ptr<float>(), nullptr, stream(dev));
         }
-        Tensor q = make_codes(x, r.n, r.d), s = make(x, {r.n}, at::kFloat);
-        check(lib.rmsnorm8(r.p, dtype(x), r.n, r.d, r.ld, o.p, o.ld, w, (float)eps, h.defined() ? h.data_ptr() : nullptr,
-                           r.d, q.data_ptr<int8_t>(), pitch_of(r.d), s.data_ptr<float>(), nullptr, stream(dev)),
-              "qamw_rmsnorm8");
+        check(rc, "qamw_rmsnorm8");
         PyObject* sum = h.defined() ? THPVariable_Wrap(std::move(h)) : Py_NewRef(a[0]);   // without a residual: x
         return tuple({THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(s)), sum});
     });
@@ -202,12 +227,17 @@ PyObject* gemm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rows x = codes(xq, dev), w = codes(wq, dev);
         if (x.d != w.d) throw Skip{};
         const float *xs = vec(tensor(a[1]), dev, x.n), *ws = vec(tensor(a[3]), dev, w.n);
-        Tensor y = make(xq, {x.n, w.n}, a[4] == Py_True ? at::kBFloat16 : at::kFloat), work;
-        const size_t need = lib.gemm8_workspace(x.n, w.n, x.d);
-        if (need) work = make(xq, {(int64_t)need}, at::kByte);
-        check(lib.gemm8((const int8_t*)x.p, x.ld, xs, x.n, (const int8_t*)w.p, w.ld, ws, w.n, x.d, y.data_ptr(), dtype(y),
-                        w.n, need ? work.data_ptr() : nullptr, need, stream(dev)),
-              "qamw_gemm8");
+        Tensor y, work;
+        int rc;
+        {
+            const Unlocked unlocked;
+            y = make(xq, {x.n, w.n}, a[4] == Py_True ? at::kBFloat16 : at::kFloat);
+            const size_t need = lib.gemm8_workspace(x.n, w.n, x.d);
+            if (need) work = make(xq, {(int64_t)need}, at::kByte);
+            rc = lib.gemm8((const int8_t*)x.p, x.ld, xs, x.n, (const int8_t*)w.p, w.ld, ws, w.n, x.d, y.data_ptr(),
+                           dtype(y), w.n, need ? work.data_ptr() : nullptr, need, stream(dev));
+        }
+        check(rc, "qamw_gemm8");
         return THPVariable_Wrap(std::move(y));
     });
 }
