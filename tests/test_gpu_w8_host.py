@@ -70,3 +70,16 @@ def test_other_threads_run_during_a_launch(q):
         assert h.gemm8(c, s, c, s, True) is not None
     finally:
         q.w8.bind(q.load())
+
+
+def test_gradients_are_not_cut_off(q):
+    """A residual stream that records gradients is refused by the compiled way too; without recording it is taken."""
+    x = torch.ones((4, 64), device=DEV)
+    for a, b in ((x.clone().requires_grad_(), x), (x, x.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="gradient"):
+            q.rmsnorm8(a, residual=b)
+        with torch.no_grad():
+            assert torch.equal(q.rmsnorm8(a, residual=b)[2], 2 * x)
+    a = x.clone().requires_grad_()
+    assert q.rmsnorm8(a)[2] is a
+    assert not q.rmsnorm8(x, torch.ones(64, device=DEV, requires_grad=True), residual=x)[2].requires_grad

@@ -1,0 +1,22 @@
+"""Calls of the 8-bit binding that are refused or answered before any device is needed."""
+import pytest
+import torch
+
+import weight_quantization_codec_amd as q
+
+
+def test_the_residual_stream_keeps_its_history():
+    """h of rmsnorm8 would carry a residual stream on, without its history: where h is not x itself, x or a residual
+    that requires a gradient is refused while gradients are recorded, and only then."""
+    x, r = torch.zeros((4, 64)), torch.zeros((4, 64))
+    with pytest.raises(ValueError, match="device"):
+        q.rmsnorm8(x.clone().requires_grad_())   # h is x, with its history
+    for kw in (dict(x=x, residual=r.clone().requires_grad_()), dict(x=x.clone().requires_grad_(), residual=r),
+               dict(x=(2 * x.clone().requires_grad_()), residual=r), dict(x=x.clone().requires_grad_(), sum_out=r)):
+        with pytest.raises(ValueError, match="gradient"):
+            q.rmsnorm8(**kw)
+        with torch.no_grad(), pytest.raises(ValueError, match="device"):
+            q.rmsnorm8(**kw)
+        kw = {k: v.detach() for k, v in kw.items()}
+        with pytest.raises(ValueError, match="device"):
+            q.rmsnorm8(weight=torch.ones(64, requires_grad=True), **kw)   # a parameter: no output carries it on

@@ -14,6 +14,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -202,7 +203,11 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
             throw Skip{};
         }
         Rows o{nullptr, 0, 0, 0};
-        if (a[3] != Py_None) o = rows(tensor(a[3]), dev, &x);
+        if (a[3] != Py_None) {
+            const Tensor& res = tensor(a[3]);
+            o = rows(res, dev, &x);
+            if (c10::GradMode::is_enabled() && (x.requires_grad() || res.requires_grad())) throw Skip{};   // refused there
+        }
         Tensor h, q, s;
         int rc;
         {

@@ -6,6 +6,9 @@ device, outputs made here) take a short way through the compiled module _w8_host
 and every other call, all errors among them, the way through this file.  Work is queued on the current stream
 of the tensors' device.  Codes are int8 tensors whose rows start on 16-byte boundaries; the functions
 that make codes return rows x d views of buffers with rows of q8_stride(d) bytes.
+
+Nothing here has a backward: codes, row scales, values read back and products carry no gradient, whatever their
+inputs require.
 """
 from __future__ import annotations
 
@@ -243,7 +246,8 @@ def rmsnorm8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
              status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Residual addition and root-mean-square norm: (int8 codes of the normalized rows, their fp32 row
     scales, h = x + residual).  Without a residual h is x itself, and sum_out (if given) a copy of it;
-    sum_out may be x or residual (h in place).  See qamw_rmsnorm8."""
+    sum_out may be x or residual (h in place).  h carries no gradient: but where it is x itself, x or residual
+    that requires one is refused while gradients are recorded.  See qamw_rmsnorm8."""
     if sum_out is None and out is None and row_scale is None and status is None and _host is not None:
         made = _host.rmsnorm8(x, weight, eps, residual)
         if made is not None:
@@ -252,6 +256,10 @@ def rmsnorm8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     rows, d = x.shape
     ld_r = _rows(residual, "residual", like=x) if residual is not None else 0
     ld_s = _rows(sum_out, "sum_out", like=x) if sum_out is not None else d
+    if (residual is not None or sum_out is not None) and torch.is_grad_enabled() and (
+            x.requires_grad or (residual is not None and residual.requires_grad)):
+        raise ValueError("%s requires a gradient, which h would cut off: call under torch.no_grad()"
+                         % ("x" if x.requires_grad else "residual"))
     if weight is not None:
         _vec(weight, "weight", d)
     if row_scale is not None:
