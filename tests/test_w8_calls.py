@@ -20,3 +20,14 @@ def test_the_residual_stream_keeps_its_history():
         kw = {k: v.detach() for k, v in kw.items()}
         with pytest.raises(ValueError, match="device"):
             q.rmsnorm8(weight=torch.ones(64, requires_grad=True), **kw)   # a parameter: no output carries it on
+
+
+def test_workspace_of_sizes_past_32_bits():
+    """Sizes that gemm8 refuses need no workspace; none is taken for another that it equals in 32 bits."""
+    need = q.gemm8_workspace(77, 4096, 11008)
+    assert need > 0
+    for past in (2**32, -2**32, 2**31, 2**63, 2**64):
+        assert q.gemm8_workspace(past + 77, 4096, 11008) == 0
+        assert q.gemm8_workspace(77, past + 4096, 11008) == 0
+        assert q.gemm8_workspace(77, 4096, past + 11008) == 0
+    assert q.gemm8_workspace(77, 4096, 11008) == need

@@ -292,7 +292,9 @@ def rmsnorm8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
 
 
 def gemm8_workspace(M: int, d_out: int, d_in: int) -> int:
-    """Bytes of workspace that gemm8 uses (0 for most sizes)."""
+    """Bytes of workspace that gemm8 uses (0 for most sizes, and for those that it refuses)."""
+    if not all(-_INT_MAX <= size <= _INT_MAX for size in (M, d_out, d_in)):   # ctypes would cut them to 32 bits
+        return 0
     return _fns["qamw_gemm8_workspace"](M, d_out, d_in)
 
 
