@@ -53,7 +53,8 @@ def build(jobs: int = 8) -> str:
 
 
 def build_host() -> str:
-    """Compile the binding's host module (csrc/w8_host.cpp) against the installed torch."""
+    """Compile the binding's host module (csrc/w8_host.cpp) against the installed torch.  Where that fails no older
+    module stays: w8.py does without one."""
     import sysconfig
 
     from torch.utils import cpp_extension
@@ -66,9 +67,15 @@ def build_host() -> str:
     for d in cpp_extension.library_paths():
         cmd += ["-L", d]
     cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("g++ failed for w8_host.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr[-4000:]))
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failure = r.stderr[-4000:] if r.returncode else None
+    except OSError as e:   # no such compiler
+        failure = str(e)
+    if failure is not None:
+        if os.path.exists(HOST):
+            os.remove(HOST)
+        raise RuntimeError("g++ failed for w8_host.cpp:\n%s\n%s" % (" ".join(cmd), failure))
     os.replace(tmp, HOST)
     return HOST
 
