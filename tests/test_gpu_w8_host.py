@@ -2,10 +2,12 @@
 with products that need a workspace."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 from helpers import DEV
+from test_gpu_w8 import _code_matrix, _want
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +85,79 @@ def test_gradients_are_not_cut_off(q):
     a = x.clone().requires_grad_()
     assert q.rmsnorm8(a)[2] is a
     assert not q.rmsnorm8(x, torch.ones(64, device=DEV, requires_grad=True), residual=x)[2].requires_grad
+
+
+# products with k in parts, whose sums wait in a workspace that the call makes
+PARTS = [(77, 4096, 11008), (200, 1024, 4096)]
+
+
+def _parts(q, seed=0):
+    rng = np.random.default_rng(seed)
+    cases = []
+    for M, N, K in PARTS:
+        assert q.gemm8_workspace(M, N, K) > 0
+        cases.append((_code_matrix(rng, M, K), torch.from_numpy(rng.random(M, dtype=np.float32)).to(DEV),
+                      _code_matrix(rng, N, K), torch.from_numpy(rng.random(N, dtype=np.float32)).to(DEV)))
+    return cases
+
+
+@pytest.mark.parametrize("od", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_products_in_parts(q, od, monkeypatch):
+    """By the compiled way, alone and through the package, and by the long way; nothing stays allocated."""
+    for case in _parts(q):
+        want = _want(*case, od)
+        assert torch.equal(q.gemm8(*case, out_dtype=od), want)
+        made = q.w8._host.gemm8(*case, od is torch.bfloat16)
+        assert made is not None and torch.equal(made, want)
+        with monkeypatch.context() as m:
+            m.setattr(q.w8, "_host", None)
+            assert torch.equal(q.gemm8(*case, out_dtype=od), want)
+        del made
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        for _ in range(50):
+            q.gemm8(*case, out_dtype=od)
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_allocated() == before
+
+
+def test_products_in_parts_on_two_streams(q):
+    """Calls that may overlap, on streams of their own: each has a workspace to itself."""
+    cases = _parts(q, 1)
+    want = [_want(*c, torch.bfloat16) for c in cases]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(12):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((q.gemm8(*cases[i // 2 % 2]), want[i // 2 % 2]))
+    torch.cuda.synchronize()
+    for i, (y, w) in enumerate(got):
+        assert torch.equal(y, w), i
+
+
+def test_products_in_parts_in_a_graph(q):
+    """Captured without a workspace of the caller's; replays with other inputs and eager calls between."""
+    cases = _parts(q, 2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c in cases:
+            q.gemm8(*c)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        made = [q.gemm8(*c) for c in cases]
+    for i in range(4):
+        for c in cases:
+            c[0].copy_(torch.randint_like(c[0], -128, 128))
+            c[1].uniform_()
+        want = [_want(*c, torch.bfloat16) for c in cases]
+        eager = [q.gemm8(*c) for c in cases]
+        torch.cuda.synchronize()
+        for y in made:
+            y.fill_(float("nan"))
+        graph.replay()
+        more = [q.gemm8(*c) for c in cases]
+        torch.cuda.synchronize()
+        for y, e, m, w in zip(made, eager, more, want):
+            assert torch.equal(y, w) and torch.equal(e, w) and torch.equal(m, w), i
