@@ -1,11 +1,11 @@
-"""The 8-bit row operators on matrices whose rows lie 2^31 bytes apart."""
+"""The 8-bit operators on matrices whose rows lie far apart."""
 import numpy as np
 import pytest
 import torch
 
 import w8_reference as ref
 from helpers import DEV, log
-from test_gpu_w8 import _same, _values
+from test_gpu_w8 import _code_matrix, _product, _same, _values, _want
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,24 @@ def test_rows_far_apart(q, dtype):
         assert np.all(np.abs(s.cpu().numpy() - s64) <= s64 * (2.0 ** -24 + 2.0 ** -36))
         _same(hs.float(), rounded(h))
         r.copy_(torch.from_numpy(b))
+
+
+# products with one matrix at the largest pitch, 2^22 bytes, and past 2^32 bytes in all: of the kernel for few rows
+# (its weights), and of 256 x 256 tiles (offsets of up to 255 rows within a tile)
+FAR_FEW = [(4, 1030, 2049), (40, 1030, 2049)]
+FAR_TILES = [(1100, 9000, 1000), (9000, 1100, 1000)]
+
+
+@pytest.mark.parametrize("M,N,K", FAR_FEW + FAR_TILES)
+def test_products_far_apart(q, M, N, K):
+    rng = np.random.default_rng(M + N)
+    x_far = M == 1100   # otherwise the weights
+    big = M if x_far else N
+    far = torch.empty((big, q.w8.GEMM8_MAX_LD), dtype=torch.int8, device=DEV)[:, :K]
+    far.copy_(_code_matrix(rng, big, K))
+    near = _code_matrix(rng, N if x_far else M, K)
+    xq, wq = (far, near) if x_far else (near, far)
+    xs, ws = torch.rand(M, device=DEV), torch.rand(N, device=DEV)
+    log("gemm8 far M=%d N=%d K=%d" % (M, N, K))
+    for od in (torch.bfloat16, torch.float32):
+        assert torch.equal(_product(q, xq, xs, wq, ws, od), _want(xq, xs, wq, ws, od))
