@@ -20,7 +20,8 @@ def _bind(q, fn):
 
 
 def _tensors():
-    return torch.ones((4, 64), device=DEV), torch.ones((4, 64), dtype=torch.int8, device=DEV), torch.ones(4, device=DEV)
+    one = lambda *s, **k: torch.ones(s, device=DEV, **k)
+    return one(4, 64), one(4, 64, dtype=torch.int8), one(4)
 
 
 def _calls(q):
@@ -161,3 +162,21 @@ def test_products_in_parts_in_a_graph(q):
         torch.cuda.synchronize()
         for y, e, m, w in zip(made, eager, more, want):
             assert torch.equal(y, w) and torch.equal(e, w) and torch.equal(m, w), i
+
+
+def test_errors_of_others_are_not_ours(q):
+    """A call answers for its own launches: an error that an earlier call of the runtime left is not its error, and
+    stays for whoever asks for it."""
+    paths = {line.split()[-1] for line in open("/proc/self/maps") if "libamdhip64" in line}
+    hip = ctypes.CDLL(paths.pop())
+    assert not paths
+    calls = _calls(q) + [lambda c=c: q.gemm8(*c) for c in _parts(q)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    for call in calls:
+        assert hip.hipSetDevice(1 << 20) != 0   # no such device: refused, and remembered
+        call()
+        assert hip.hipGetLastError() != 0
+        assert hip.hipGetLastError() == 0
+    torch.cuda.synchronize()

@@ -418,6 +418,7 @@ hipError_t allow_big_lds(K kernel, int bytes, std::atomic<uint64_t>& done) {
     if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    else (void)hipGetLastError();
     return e;
 }
 
@@ -428,9 +429,8 @@ hipError_t launch_tile_kernel(const Gemm8Args& a, int tiles_m, int tiles_n, int 
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_big_lds(kernel, C::kLds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n * splits)), dim3(256), C::kLds, st, a, tiles_m,
-                       tiles_n, splits);
-    return hipGetLastError();
+    return launch_kernel(kernel, dim3((unsigned)(tiles_m * tiles_n * splits)), 256, C::kLds, st, a, tiles_m, tiles_n,
+                         splits);
 }
 
 template <int BM, int BN, int WM, int KS, int S, int SP, int FA>
@@ -448,11 +448,7 @@ hipError_t launch_tiles_or_parts(const Gemm8Args& a, int splits, hipStream_t st)
     const hipError_t e = launch_tile_kernel<BM, BN, WM, KS, S, SP, FA, kSums>(a, tiles_m, tiles_n, splits, st);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)(((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256));
-    if (a.y_bf16)
-        hipLaunchKernelGGL((k_gemm8_join<true>), grid, dim3(256), 0, st, a, splits);
-    else
-        hipLaunchKernelGGL((k_gemm8_join<false>), grid, dim3(256), 0, st, a, splits);
-    return hipGetLastError();
+    return launch_kernel(a.y_bf16 ? k_gemm8_join<true> : k_gemm8_join<false>, grid, 256, 0, st, a, splits);
 }
 
 // Few activation rows: bound by the one read of the weights.  A workgroup has up to 32 weight rows, as many
@@ -558,8 +554,7 @@ hipError_t launch_thin_kernel(const Gemm8Args& a, hipStream_t st) {
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_big_lds(kernel, kLds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(W * kWave), kLds, st, a, rows);
-    return hipGetLastError();
+    return launch_kernel(kernel, dim3((unsigned)((a.N + rows - 1) / rows)), W * kWave, kLds, st, a, rows);
 }
 
 // 4 wavefronts, and as many units in flight as leave room for two workgroups a compute unit (up to 32

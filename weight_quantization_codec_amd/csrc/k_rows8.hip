@@ -339,9 +339,8 @@ hipError_t launch_rows_v(const Rows8Args& a, int w, hipStream_t st) {
     int64_t wgs = ((int64_t)a.rows + rows_wg - 1) / rows_wg;
     const int64_t most = keep ? 256 * (12 / (rows_wg * w) > 0 ? 12 / (rows_wg * w) : 1) : 1 << 20;
     wgs = wgs < most ? wgs : most;
-    hipLaunchKernelGGL((k_rows8<KIND, BF, FACTOR, V>), dim3((unsigned)wgs), dim3(rows_wg * w * kWave), keep ? bytes : 0,
-                       st, a, w, keep ? 1 : 0);
-    return hipGetLastError();
+    return launch_kernel(k_rows8<KIND, BF, FACTOR, V>, dim3((unsigned)wgs), rows_wg * w * kWave, keep ? bytes : 0, st, a,
+                         w, keep ? 1 : 0);
 }
 
 template <int KIND, bool BF, bool FACTOR>
@@ -435,8 +434,7 @@ hipError_t launch_dequant(const Dequant8Args& a, hipStream_t st) {
     const int64_t rows_wg = 256 / tx, tiles = (a.rows + rows_wg - 1) / rows_wg;
     const int64_t cols = (chunks + tx - 1) / tx, most = (2048 + cols - 1) / cols;   // 8 workgroups a compute unit
     const dim3 grid((unsigned)cols, (unsigned)(tiles < most ? tiles : most));
-    hipLaunchKernelGGL((k_dequant8<BF, SCALE>), grid, dim3(256), 0, st, a, tx);
-    return hipGetLastError();
+    return launch_kernel(k_dequant8<BF, SCALE>, grid, 256, 0, st, a, tx);
 }
 
 }  // namespace

@@ -7,6 +7,19 @@
 
 namespace qamw {
 
+// Launches a kernel and gives that launch's own error.  (hipGetLastError would also give an error that an earlier
+// call of the thread has left.)  An error that is given here is not left for others.
+template <typename... P, typename... A>
+hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, int block, size_t lds, hipStream_t st, A... args) {
+    auto launch = [&](P... values) {
+        void* p[] = {&values...};
+        return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3((unsigned)block), p, lds, st);
+    };
+    const hipError_t e = launch(args...);
+    if (e != hipSuccess) (void)hipGetLastError();
+    return e;
+}
+
 // Rows to codes (k_rows8.hip): plain, gated, or behind a norm.
 struct Rows8Args {
     const void* x;
