@@ -26,7 +26,8 @@ def _tensors():
 
 def _calls(q):
     x, c, s = _tensors()
-    return [lambda: q.quant8(x), lambda: q.dequant8(c, s), lambda: q.rmsnorm8(x, residual=x), lambda: q.gemm8(c, s, c, s)]
+    return [lambda: q.quant8(x), lambda: q.dequant8(c, s), lambda: q.rmsnorm8(x, residual=x),
+            lambda: q.gemm8(c, s, c, s)]
 
 
 @pytest.mark.parametrize("which", range(4), ids=["quant8", "dequant8", "rmsnorm8", "gemm8"])

@@ -10,7 +10,8 @@
 // Bound by HBM.  Measured (bytes of the rows and codes, against 5.1 TB/s of a large copy): norm with
 // residual, 4096 x 5120 bf16, 28.6 us (5.1 TB/s); weights with channel scale, 13824 x 5120 bf16, 47 us
 // (4.5 TB/s; 54 with the scales read again for every row, 42 without a scale); gated 2048 x 13824 bf16, 31 us
-// (4.6 TB/s); dequant8 of 13824 x 5120 with channel scale 37 us (5.7 TB/s, part of the codes still in cache).
+// (4.6 TB/s); dequant8 of 13824 x 5120 with channel scale 37 us (5.7 TB/s, part of the codes still in cache; 46.6 us
+// from memory; to fp32 147 us, 2.4 TB/s).
 // A single row takes 2.7 to 3.4 us, most of it the launch.
 //
 // Rounding.  Values are fp32 from the load on; the sum of squares is fp64, which holds the square of

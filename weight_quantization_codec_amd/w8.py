@@ -5,7 +5,8 @@ The binding marshals arguments as the rest of the package does; ordinary calls (
 device, outputs made here) take a short way through the compiled module _w8_host, with the same checks,
 and every other call, all errors among them, the way through this file.  Work is queued on the current stream
 of the tensors' device.  Codes are int8 tensors whose rows start on 16-byte boundaries; the functions
-that make codes return rows x d views of buffers with rows of q8_stride(d) bytes.
+that make codes return rows x d views of buffers with rows of q8_stride(d) bytes, and write zeros up to the next
+multiple of 16 bytes behind each row, in a given out too.
 
 Nothing here has a backward: codes, row scales, values read back and products carry no gradient, whatever their
 inputs require.
