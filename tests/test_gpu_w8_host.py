@@ -1,6 +1,7 @@
 """The compiled short way of the 8-bit binding: what it does with failures, with the interpreter lock, and
 with products that need a workspace."""
 import ctypes
+import gc
 
 import numpy as np
 import pytest
@@ -52,6 +53,7 @@ def test_memory_that_is_not_there_is_asked_for_once(q):
     s = torch.ones(1 << 16, device=DEV)
     ooms = lambda: torch.cuda.memory_stats()["num_ooms"]
     before = ooms()
+    torch.cuda.empty_cache()   # no block that would do is kept from earlier
     torch.cuda.set_per_process_memory_fraction(0.02)   # of 288 GB; the output takes 17
     try:
         with pytest.raises(torch.OutOfMemoryError):
@@ -115,6 +117,7 @@ def test_products_in_parts(q, od, monkeypatch):
             m.setattr(q.w8, "_host", None)
             assert torch.equal(q.gemm8(*case, out_dtype=od), want)
         del made
+        gc.collect()   # tensors that errors of earlier calls still hold, or they go during the count
         torch.cuda.synchronize()
         before = torch.cuda.memory_allocated()
         for _ in range(50):

@@ -311,7 +311,7 @@ __global__ __launch_bounds__(max_waves(V) * kWave) void k_rows8(Rows8Args a, int
 // twice the bytes, 4 (8 chunks of fp32 do not fit the registers of 8 wavefronts, and a kernel with scratch
 // memory takes 12 us longer to start: for the widest rows only).  Less work is spread over more wavefronts: 2
 // chunks below 3 million values (512 x 4096 norm bf16: 2 chunks 6.1 us, 4: 6.8; 1000 x 6336: 15.3 and 12.7), 1 for
-// up to 256 rows (256 x 2048: 3.8 us, 2: 4.1).
+// up to 256 rows (256 x 2048: 3.8 us, 2: 4.1).  Each threshold rests on the sizes named with it, no more.
 struct RowShape {
     int v, w;
 };
