@@ -2,6 +2,7 @@
 with products that need a workspace."""
 import ctypes
 import gc
+import threading
 
 import numpy as np
 import pytest
@@ -184,3 +185,30 @@ def test_errors_of_others_are_not_ours(q):
         assert hip.hipGetLastError() != 0
         assert hip.hipGetLastError() == 0
     torch.cuda.synchronize()
+
+
+def test_calls_of_several_threads(q):
+    """Threads with a stream each, whose calls overlap on the host and on the GPU."""
+    cases = _parts(q, 3) + [_parts(q, 4)[1]]
+    want = [_want(*c, torch.bfloat16) for c in cases]
+    x = [torch.randn((50 + i, 1003), device=DEV) for i in range(len(cases))]
+    rows = [q.quant8(v) for v in x]
+    torch.cuda.synchronize()
+    wrong, done = [], []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(40):
+                y, (c, s) = q.gemm8(*cases[i]), q.quant8(x[i])
+                if not (torch.equal(y, want[i]) and torch.equal(c, rows[i][0]) and torch.equal(s, rows[i][1])):
+                    wrong.append(i)
+        stream.synchronize()
+        done.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and sorted(done) == [0, 1, 2]
