@@ -9,10 +9,9 @@
 // where the tiles do not fill the chip, k is split over workgroups too and k_gemm8_join adds their sums.
 // k_gemm8_thin, for few activation rows, spreads the weight rows evenly over the compute units and splits k
 // over the wavefronts of a workgroup.  plan() (qamw_w8_plan.hpp) chooses.
-#include <atomic>
-#include <type_traits>
-
 #include "qamw_device.hpp"
+#include "qamw_rows.hpp"
+#include "qamw_tile.hpp"
 #include "qamw_w8_launch.hpp"
 #include "qamw_w8_plan.hpp"
 
@@ -22,71 +21,9 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// f(0), .., f(N - 1) with the index a compile-time constant.
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-    if constexpr (I < N) {
-        f(std::integral_constant<int, I>{});
-        static_for<N, I + 1>(f);
-    }
-}
-
-// 16 bytes of output at any alignment of its elements
-struct __attribute__((packed, aligned(2))) Out16 {
-    uint32_t w[4];
-};
-
-struct __attribute__((packed, aligned(2))) Out8 {
-    uint32_t w[2];
-};
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    const uint32_t a = __builtin_bit_cast(uint16_t, (__bf16)lo), b = __builtin_bit_cast(uint16_t, (__bf16)hi);
-    return a | (b << 16);
-}
-
-// 16 bytes a lane from a buffer into LDS at lds + 16 lane (lds uniform), without registers between.
-// Written as assembly: the compiler would wait for every such load before any read of LDS, while the
-// kernel knows which stage a load fills and waits for that one (wait_stage).  The instruction has no
-// register output; M0, which nothing else in these kernels uses, needs one wait state before it.
-__device__ __forceinline__ void load_lds16(u32x4 rsrc, uint32_t voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory");
-}
-
-// A buffer descriptor: `size` bytes from `base` on, loads past them give zeros.
-__device__ __forceinline__ u32x4 rsrc_of(uint64_t base, uint32_t size) {
-    u32x4 r;
-    r[0] = __builtin_amdgcn_readfirstlane((uint32_t)base);
-    r[1] = __builtin_amdgcn_readfirstlane((uint32_t)(base >> 32) & 0xFFFFu);
-    r[2] = __builtin_amdgcn_readfirstlane(size);
-    r[3] = 0x00020000u;
-    return r;
-}
-
-// Waits until at most N of the wavefront's loads and none of its LDS reads are under way, then for the
-// workgroup.
-template <int N>
-__device__ __forceinline__ void wait_stage() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
-// The same for LDS reads alone: behind it the workgroup has read what it has asked for.
-__device__ __forceinline__ void wait_reads() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 // What a tile leaves: y, or its sums over a part of k, to be joined.
 enum { kF32 = 0, kBf16 = 1, kSums = 2 };
-__host__ __device__ constexpr int sums_pitch(int n) { return (n + 63) / 64 * 64; }
 
 // A tile of BM activation rows by BN weight rows, WM x 4 / WM wavefronts, S stages of KS bytes of k in LDS.
 //
@@ -122,21 +59,6 @@ struct TileCfg {
         return n;
     }
 };
-
-// The workgroup's tile.  Workgroups go round the 8 XCDs; each XCD gets a contiguous run of tiles, taken
-// kGroup tile rows at a time, so that the tiles an XCD works on at once share rows in its L2.
-constexpr int kXcds = 8, kGroup = 8;
-__device__ __forceinline__ int tile_of(int b, int splits, int tiles_m, int tiles_n, int& tm, int& tn) {
-    const int tiles = tiles_m * tiles_n, all = tiles * splits, per = all / kXcds, rest = all % kXcds, x = b % kXcds;
-    int t = x * per + (x < rest ? x : rest) + b / kXcds;
-    const int split = t / tiles;
-    t -= split * tiles;
-    const int group = t / (kGroup * tiles_n), first = group * kGroup;
-    const int in = tiles_m - first < kGroup ? tiles_m - first : kGroup, at = t - first * tiles_n;
-    tm = first + at % in;
-    tn = at / in;
-    return split;
-}
 
 template <int BM, int BN, int WM, int KS, int S, int SP, int FA, int OUT>
 __global__ __launch_bounds__(256, 1) void k_gemm8(Gemm8Args a, int tiles_m, int tiles_n, int splits) {
@@ -405,21 +327,6 @@ __global__ __launch_bounds__(256) void k_gemm8_join(Gemm8Args a, int splits) {
         for (int e = 0; e < 4; ++e)
             if (n + e < a.N) y[e] = v[e];
     }
-}
-
-// Lets a kernel use more than the default 64 KiB of LDS on the current device; `done` has a bit for each
-// device where that has been said.
-template <typename K>
-hipError_t allow_big_lds(K kernel, int bytes, std::atomic<uint64_t>& done) {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    else (void)hipGetLastError();
-    return e;
 }
 
 template <int BM, int BN, int WM, int KS, int S, int SP, int FA, int OUT>

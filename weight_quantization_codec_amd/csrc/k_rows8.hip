@@ -17,97 +17,17 @@
 // Rounding.  Values are fp32 from the load on; the sum of squares is fp64, which holds the square of
 // every fp32 value and adds 32768 of them without overflow or loss that matters.  NaN counts as larger
 // than every number in the row's maximum, and so reaches the row's flag.
-#include <type_traits>
-
 #include "qamw.h"
 #include "qamw_device.hpp"
+#include "qamw_rows.hpp"
 #include "qamw_w8_launch.hpp"
 
 namespace qamw {
 
 namespace {
 
-constexpr int kChunk = 8;            // columns of a chunk
 constexpr int kMaxWaves = 16;
 constexpr float kZeroRow = 0x1p-119f;   // rows below this are zero rows: 127 / top stays finite
-
-// 16 bytes at any address that the element type allows: gfx950 loads and stores wide at any alignment
-struct __attribute__((packed, aligned(2))) Bytes16 {
-    uint32_t w[4];
-};
-struct __attribute__((packed, aligned(4))) Float8 {
-    float v[8];
-};
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    const uint32_t a = __builtin_bit_cast(uint16_t, (__bf16)lo), b = __builtin_bit_cast(uint16_t, (__bf16)hi);
-    return a | (b << 16);   // v_cvt_pk_bf16_f32: round to nearest even
-}
-
-// The 8 columns of a chunk as they are stored, at any alignment of the elements.
-template <bool BF>
-using Raw = std::conditional_t<BF, Bytes16, Float8>;
-
-template <bool BF>
-__device__ __forceinline__ const void* at(const void* p, int64_t element) {
-    return reinterpret_cast<const char*>(p) + element * (BF ? 2 : 4);
-}
-
-template <bool BF>
-__device__ __forceinline__ void unpack(const Raw<BF>& b, float (&v)[kChunk]) {
-    if constexpr (BF) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(b.w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(b.w[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) v[i] = b.v[i];
-    }
-}
-
-// The first n < 8 columns of a chunk, and zeros.
-template <bool BF>
-__device__ __forceinline__ void load_part(const void* p, int n, float (&v)[kChunk]) {
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-        v[i] = 0.0f;
-        if (i < n) {
-            if constexpr (BF)
-                v[i] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[i]);
-            else
-                v[i] = reinterpret_cast<const float*>(p)[i];
-        }
-    }
-}
-
-template <bool BF>
-__device__ __forceinline__ void store_chunk(void* y, const float (&v)[kChunk]) {
-    if constexpr (BF) {
-        Bytes16 b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b.w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<Bytes16*>(y) = b;
-    } else {
-        Float8 b;
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) b.v[i] = v[i];
-        *reinterpret_cast<Float8*>(y) = b;
-    }
-}
-
-template <bool BF>
-__device__ __forceinline__ void store_part(void* y, int n, const float (&v)[kChunk]) {
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i)
-        if (i < n) {
-            if constexpr (BF)
-                reinterpret_cast<uint16_t*>(y)[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
-            else
-                reinterpret_cast<float*>(y)[i] = v[i];
-        }
-}
 
 // silu(g) = g / (1 + exp(-g)).  v_exp_f32 and v_rcp_f32 are within an ulp; the rounded product
 // -g log2(e) adds |g| 2^-24 of the exponential.  exp(-g) overflows to infinity below -88: -0 there.
@@ -117,11 +37,6 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 enum { kPlain = 0, kGated = 1, kNorm = 2 };
-
-// The larger of a magnitude and |v|; NaN if either is (v_maximum3_f32).
-__device__ __forceinline__ float top_of(float top, float v) {
-    return __builtin_elementwise_maximum(top, __builtin_fabsf(v));
-}
 
 // Codes of 8 values: fl32(v back) is at most 127; adding 1.5 2^23 rounds it to the nearest whole number,
 // ties to even, and leaves that as two's complement in the low bits.
