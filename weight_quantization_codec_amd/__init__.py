@@ -18,7 +18,10 @@ from typing import Dict, Optional
 
 import torch
 
+from . import mx4 as _mx4
 from . import w8 as _w8
+from .mx4 import (dequant4, gemm4, gemm4_grouped, gemm4_workspace, mx4_groups, mx4_stride, quant4,  # noqa: F401
+                  rmsnorm4)
 from .w8 import dequant8, gemm8, gemm8_workspace, q8_stride, quant8, rmsnorm8  # noqa: F401
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +29,7 @@ ROOT = os.path.dirname(PKG_DIR)
 LIB_PATH = os.path.join(PKG_DIR, "libqamw.so")
 HEADER_PATH = os.path.join(ROOT, "include", "qamw.h")
 W8_HEADER_PATH = os.path.join(ROOT, "include", "qamw_w8.h")
+MX4_HEADER_PATH = os.path.join(ROOT, "include", "qamw_mx4.h")
 
 F32, BF16 = 0, 1
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = 0, -1, -2, -3, -4
@@ -87,7 +91,7 @@ def load(path: Optional[str] = None):
                                vp], ctypes.c_int),
         "qamw_status_string": ([ctypes.c_int], ctypes.c_char_p),
     }
-    for name, (args, res) in list(sig.items()) + list(_w8.SIGNATURES.items()):
+    for name, (args, res) in list(sig.items()) + list(_w8.SIGNATURES.items()) + list(_mx4.SIGNATURES.items()):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res

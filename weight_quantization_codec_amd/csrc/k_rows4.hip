@@ -1,0 +1,393 @@
+// Rows of a matrix as 4-bit codes with a power of two for every 32 columns (quant4, rmsnorm4), and back
+// (dequant4).
+//
+// A lane has 8 consecutive columns (a chunk), four lanes have a block: its largest magnitude takes two exchanges
+// within the four.  The power of two comes from the exponent bits of that magnitude, so dividing by it is
+// exact and v_cvt_scalef32_pk_fp4_f32 (ties to the even code, saturating) gives the codes of the exact
+// quotients.  Nothing of a row is needed for a block: quant4 streams, each lane over rows of the same columns;
+// rmsnorm4 holds a row in the registers of 1 to 16 wavefronts, for its sum of squares.
+#include "qamw.h"
+#include "qamw_device.hpp"
+#include "qamw_mx4_launch.hpp"
+#include "qamw_rows.hpp"
+
+namespace qamw {
+
+namespace {
+
+constexpr int kMaxWaves = 16;
+constexpr int kGroupChunks = kGroupCols / kChunk;
+constexpr float kZeroBlock = 0x1p-119f;   // blocks below this are zero blocks: every power of two used is normal
+
+// Lane l's value from the lane that control C names, within rows of 16 lanes.
+template <int C>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, C, 0xF, 0xF, true);
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E;   // quad_perm [1,0,3,2] and [2,3,0,1]
+constexpr int kRor4 = 0x124, kRor8 = 0x128;   // row_ror
+
+// A chunk of a block as codes: its 4 bytes, and in `scale` the block's byte.  The four lanes of the block call this
+// together.
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[kChunk], uint32_t& scale, bool& bad) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) top = top_of(top, v[i]);
+    top = top_of(top, __uint_as_float(dpp<kSwap1>(__float_as_uint(top))));
+    top = top_of(top, __uint_as_float(dpp<kSwap2>(__float_as_uint(top))));
+    bad = !(top < __builtin_inff());
+    const bool zero = bad || top < kZeroBlock;
+    // top = m 2^x with 1 <= m < 2: the exponent is x - 2 up to m = 1.75 and x - 1 above
+    const uint32_t byte = ((__float_as_uint(top) + 0x1FFFFFu) >> 23) - 2;
+    scale = bad ? 255u : zero ? 0u : byte;
+    const float unit = __uint_as_float(byte << 23);
+    uint32_t q = 0;
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], unit, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], unit, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], unit, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], unit, 3);
+    return zero ? 0u : q;
+}
+
+// Writes chunk c of a row and, of 16 lanes (chunks c & -16 .. c | 15), one the four scale bytes.
+__device__ __forceinline__ void store_codes(const Rows4Args& a, int64_t row, int c, uint32_t q, uint32_t scale) {
+    *reinterpret_cast<uint32_t*>(a.q + row * a.ld_q + c * 4) = q;
+    uint32_t s = scale << (8 * (c / 4 % 4));
+    s |= dpp<kRor4>(s);
+    s |= dpp<kRor8>(s);
+    if (c % 16 == 0)
+        *reinterpret_cast<uint32_t*>(a.e + c / kGroupChunks * a.ld_e + row * 8 + c / 16 % 2 * 4) = s;
+}
+
+// x g / (1 + exp(-g)) in fp64, rounded to fp32 once.  exp(-g) = 2^n 2^f with |f| <= 1/2, and 2^f by the polynomial of
+// degree 8 through the Chebyshev nodes of that interval (within 2^-39.7 of itself).  With n held to +-1000, a
+// quotient below every fp32 number stays one, and an infinite g gives an infinite or undefined product.
+__device__ __forceinline__ float gated(float x, float g) {
+    const double p = (double)x * (double)g, t = (double)g * -1.4426950408889634;
+    const double n = __builtin_rint(t), f = t - n;
+    double e = 1.3255224887502117e-06;
+    e = __builtin_fma(e, f, 1.531007940254368e-05);
+    e = __builtin_fma(e, f, 0.0001540345585240991);
+    e = __builtin_fma(e, f, 0.0013333450567999414);
+    e = __builtin_fma(e, f, 0.009618129159402628);
+    e = __builtin_fma(e, f, 0.05550410941205934);
+    e = __builtin_fma(e, f, 0.2402265069581299);
+    e = __builtin_fma(e, f, 0.6931471805459335);
+    e = __builtin_fma(e, f, 1.0);
+    const double held = __builtin_fmin(__builtin_fmax(n, -1000.0), 1000.0);
+    const double d = 1.0 + __builtin_ldexp(e, (int)held);
+    double r = __builtin_amdgcn_rcp(d);   // within 2^-20 or better; two steps of Newton's iteration
+    r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+    r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+    return (float)(p * r);
+}
+
+// 8 columns a thread; a workgroup covers tx chunks of rows_wg rows, 256 / tx at a time, and keeps the channel
+// scales of its columns over its rows.
+template <bool BF, bool GATE, bool SCALE>
+__global__ __launch_bounds__(256) void k_quant4(Rows4Args a, int tx, int rows_wg) {
+    const int c = blockIdx.x * tx + threadIdx.x % tx, ty = 256 / tx, j = c * kChunk;
+    // (tx and the chunks of a row are multiples of 32: the lanes of a block, and the 16 of a store, leave together)
+    if (c >= (a.d + kGroupCols - 1) / kGroupCols * kGroupChunks) return;
+    const int have = a.d - j;   // columns of the chunk: below 8 in the last one, none behind it
+    float f[kChunk];
+    if constexpr (SCALE) {
+        if (have >= kChunk)
+            unpack<false>(*reinterpret_cast<const Float8*>(a.factor + j), f);
+        else
+            load_part<false>(a.factor + j, have, f);
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) bad |= i < have && !(f[i] > 0.0f);
+        if (bad && blockIdx.y == 0 && a.status) atomicOr(a.status, QAMW_FLAG_BAD_SCALE);
+    }
+    const int64_t first = (int64_t)blockIdx.y * rows_wg, end = first + rows_wg < a.rows ? first + rows_wg : a.rows;
+    bool flag = false;
+    auto write = [&](int64_t row, float (&v)[kChunk], const float (&g)[kChunk]) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            if constexpr (GATE) v[i] = gated(v[i], g[i]);
+            if constexpr (SCALE) v[i] *= f[i];
+        }
+        uint32_t s;
+        bool bad;
+        const uint32_t q = codes_of(v, s, bad);
+        flag |= bad;
+        store_codes(a, row, c, q, s);
+    };
+    int64_t row = first + threadIdx.x / tx;
+    if (have >= kChunk) {
+        // four rows at a time, every load under way before the first is used
+        constexpr int U = 4;
+        for (; row + (U - 1) * ty < end; row += U * ty) {
+            Raw<BF> x[U], o[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                x[u] = *reinterpret_cast<const Raw<BF>*>(at<BF>(a.x, (row + u * ty) * a.ld_x + j));
+                if constexpr (GATE) o[u] = *reinterpret_cast<const Raw<BF>*>(at<BF>(a.other, (row + u * ty) * a.ld_other + j));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float v[kChunk], g[kChunk];
+                unpack<BF>(x[u], v);
+                if constexpr (GATE) unpack<BF>(o[u], g);
+                write(row + u * ty, v, g);
+            }
+        }
+    }
+    for (; row < end; row += ty) {
+        float v[kChunk], g[kChunk];
+        if (have >= kChunk) {
+            unpack<BF>(*reinterpret_cast<const Raw<BF>*>(at<BF>(a.x, row * a.ld_x + j)), v);
+            if constexpr (GATE) unpack<BF>(*reinterpret_cast<const Raw<BF>*>(at<BF>(a.other, row * a.ld_other + j)), g);
+        } else {
+            load_part<BF>(at<BF>(a.x, row * a.ld_x + j), have, v);
+            if constexpr (GATE) load_part<BF>(at<BF>(a.other, row * a.ld_other + j), have, g);
+        }
+        write(row, v, g);
+    }
+    if (flag && a.status) atomicOr(a.status, QAMW_FLAG_NONFINITE);
+}
+
+// Threads across a row: a power of two from 32 to 256 that leaves few of them without a chunk.
+int across(int chunks) {
+    int tx = 32;
+    for (int wide = 64; wide <= 256; wide *= 2)
+        if ((chunks + wide - 1) / wide * wide <= (chunks + tx - 1) / tx * tx) tx = wide;
+    return tx;
+}
+
+template <bool BF, bool GATE, bool SCALE>
+hipError_t launch_quant(const Rows4Args& a, hipStream_t st) {
+    const int chunks = (a.d + kGroupCols - 1) / kGroupCols * kGroupChunks, tx = across(chunks), ty = 256 / tx;
+    const int64_t cols = (chunks + tx - 1) / tx, most = (2048 + cols - 1) / cols;   // 8 workgroups a compute unit
+    int64_t rows_wg = (a.rows + most - 1) / most;
+    rows_wg = (rows_wg + ty - 1) / ty * ty;
+    if (rows_wg > 16) rows_wg = (rows_wg + 15) / 16 * 16;   // whole lines of scales
+    const dim3 grid((unsigned)cols, (unsigned)((a.rows + rows_wg - 1) / rows_wg));
+    return launch_kernel(k_quant4<BF, GATE, SCALE>, grid, 256, 0, st, a, tx, (int)rows_wg);
+}
+
+template <bool BF>
+hipError_t launch_quant(const Rows4Args& a, hipStream_t st) {
+    if (a.other) return a.factor ? launch_quant<BF, true, true>(a, st) : launch_quant<BF, true, false>(a, st);
+    return a.factor ? launch_quant<BF, false, true>(a, st) : launch_quant<BF, false, false>(a, st);
+}
+
+// Wavefronts of a workgroup, and with them registers of a lane, by the registers that v chunks need.
+constexpr int max_waves(int v) { return v <= 2 ? 16 : v <= 4 ? 12 : 8; }
+
+// row_waves wavefronts a row: one row a workgroup, or, with one wavefront a row, blockDim / 64.  Chunk t + k threads
+// of a row is thread t's; a thread without one at some k loads the last whole one again, so that every load is
+// unconditional.
+template <bool BF, bool FACTOR, int V>
+__global__ __launch_bounds__(max_waves(V) * kWave) void k_rmsnorm4(Rows4Args a, int row_waves) {
+    __shared__ double s_sum[2][kMaxWaves];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int rows_wg = blockDim.x / kWave / row_waves, part = wave % row_waves;
+    const int t = part * kWave + lane, nt = row_waves * kWave;
+    const int full = a.d / kChunk, rest = a.d % kChunk, chunks = (a.d + kGroupCols - 1) / kGroupCols * kGroupChunks;
+    bool flag = false;
+    int buf = 0;
+    for (int64_t row = (int64_t)blockIdx.x * rows_wg + wave / row_waves; row < a.rows;
+         row += (int64_t)gridDim.x * rows_wg, buf ^= 1) {
+        const void* x = at<BF>(a.x, row * a.ld_x);
+        const void* other = at<BF>(a.other, row * a.ld_other);
+        void* sum_out = const_cast<void*>(at<BF>(a.sum, row * a.ld_sum));
+        float v[V][kChunk];
+        if (full > 0) {
+            Raw<BF> rx[V], ro[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int c = t + k * nt < full ? t + k * nt : full - 1;
+                rx[k] = *reinterpret_cast<const Raw<BF>*>(at<BF>(x, c * kChunk));
+            }
+            if (a.other) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const int c = t + k * nt < full ? t + k * nt : full - 1;
+                    ro[k] = *reinterpret_cast<const Raw<BF>*>(at<BF>(other, c * kChunk));
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k) unpack<BF>(rx[k], v[k]);
+            if (a.other) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    float o[kChunk];
+                    unpack<BF>(ro[k], o);
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) v[k][i] += o[i];
+                }
+            }
+        }
+        // the chunk that the row ends in, and the ones behind it
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = t + k * nt;
+            if (c < full) continue;
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) v[k][i] = 0.0f;
+            if (c == full && rest) {
+                load_part<BF>(at<BF>(x, c * kChunk), rest, v[k]);
+                if (a.other) {
+                    float o[kChunk];
+                    load_part<BF>(at<BF>(other, c * kChunk), rest, o);
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) v[k][i] += o[i];
+                }
+            }
+        }
+        if (a.sum) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int c = t + k * nt;
+                void* y = const_cast<void*>(at<BF>(sum_out, c * kChunk));
+                if (c < full)
+                    store_chunk<BF>(y, v[k]);
+                else if (c == full && rest)
+                    store_part<BF>(y, rest, v[k]);
+            }
+        }
+        double sum = 0.0;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) sum = __builtin_fma((double)v[k][i], (double)v[k][i], sum);
+        if constexpr (FACTOR) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int c = t + k * nt;
+                float f[kChunk];
+                if (c < full) {
+                    unpack<false>(*reinterpret_cast<const Float8*>(a.factor + c * kChunk), f);
+                } else {
+                    load_part<false>(a.factor + c * kChunk, c == full ? rest : 0, f);
+                }
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) v[k][i] *= f[i];
+            }
+        }
+#pragma unroll
+        for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+        if (row_waves > 1) {   // then the workgroup has one row
+            // two buffers by turns: a wave may be one row ahead of the slowest, never two
+            if (lane == 0) s_sum[buf][wave] = sum;
+            __syncthreads();
+            sum = s_sum[buf][0];
+            for (int w = 1; w < row_waves; ++w) sum += s_sum[buf][w];
+        }
+        const float f = (float)(1.0 / sqrt(sum / (double)a.d + a.eps));
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = t + k * nt;
+            if (c >= chunks) break;   // (of 32 lanes all or none)
+            // behind the row: zeros, whatever the factor is
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) v[k][i] = c < full || (c == full && i < rest) ? v[k][i] * f : 0.0f;
+            uint32_t s;
+            bool bad;
+            const uint32_t q = codes_of(v[k], s, bad);
+            flag |= bad;
+            store_codes(a, row, c, q, s);
+        }
+    }
+    if (flag && a.status) atomicOr(a.status, QAMW_FLAG_NONFINITE);
+}
+
+template <bool BF, bool FACTOR, int V>
+hipError_t launch_norm(const Rows4Args& a, int w, hipStream_t st) {
+    const int rows_wg = w == 1 ? 4 : 1;
+    int64_t wgs = ((int64_t)a.rows + rows_wg - 1) / rows_wg;
+    wgs = wgs < (1 << 20) ? wgs : 1 << 20;
+    return launch_kernel(k_rmsnorm4<BF, FACTOR, V>, dim3((unsigned)wgs), rows_wg * w * kWave, 0, st, a, w);
+}
+
+template <bool BF, bool FACTOR>
+hipError_t launch_norm(const Rows4Args& a, hipStream_t st) {
+    const int chunks = (a.d + kGroupCols - 1) / kGroupCols * kGroupChunks, waves = (chunks + kWave - 1) / kWave;
+    if (waves <= 8) return launch_norm<BF, FACTOR, 1>(a, waves, st);
+    if (waves <= 32) return launch_norm<BF, FACTOR, 2>(a, (waves + 1) / 2, st);
+    if (waves <= 48) return launch_norm<BF, FACTOR, 4>(a, (waves + 3) / 4, st);
+    return launch_norm<BF, FACTOR, 8>(a, (waves + 7) / 8, st);   // up to 32768 columns
+}
+
+// 8 codes a thread; a workgroup covers tx chunks of rows_wg rows, 256 / tx at a time, and keeps the reciprocals of its
+// columns' channel scales over its rows.
+template <bool BF, bool SCALE>
+__global__ __launch_bounds__(256) void k_dequant4(Dequant4Args a, int tx, int rows_wg) {
+    const int c = blockIdx.x * tx + threadIdx.x % tx, ty = 256 / tx, j = c * kChunk, have = a.d - j;
+    if (have <= 0) return;
+    float rec[kChunk];
+    if constexpr (SCALE) {
+        if (have >= kChunk)
+            unpack<false>(*reinterpret_cast<const Float8*>(a.scale + j), rec);
+        else
+            load_part<false>(a.scale + j, have, rec);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) rec[i] = 1.0f / rec[i];
+    }
+    const int64_t first = (int64_t)blockIdx.y * rows_wg, end = first + rows_wg < a.rows ? first + rows_wg : a.rows;
+    const uint8_t* e = a.e + c / kGroupChunks * a.ld_e + c / 4 % 8;
+    auto write = [&](int64_t row, uint32_t q, uint32_t byte) {
+        // 2^-127 is no normal number; 255 is NaN
+        const float unit = __uint_as_float(byte == 255 ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1),
+                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3)};
+        float v[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            v[i] = p[i / 2][i % 2] * unit;
+            if constexpr (SCALE) v[i] *= rec[i];
+        }
+        void* y = const_cast<void*>(at<BF>(a.out, row * a.ld_out + j));
+        if (have >= kChunk)
+            store_chunk<BF>(y, v);
+        else
+            store_part<BF>(y, have, v);
+    };
+    int64_t row = first + threadIdx.x / tx;
+    // four rows at a time, every load under way before the first is used
+    constexpr int U = 4;
+    for (; row + (U - 1) * ty < end; row += U * ty) {
+        uint32_t q[U], s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            q[u] = *reinterpret_cast<const uint32_t*>(a.q + (row + u * ty) * a.ld_q + c * 4);
+            s[u] = e[(row + u * ty) * 8];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) write(row + u * ty, q[u], s[u]);
+    }
+    for (; row < end; row += ty)
+        write(row, *reinterpret_cast<const uint32_t*>(a.q + row * a.ld_q + c * 4), e[row * 8]);
+}
+
+template <bool BF, bool SCALE>
+hipError_t launch_dequant(const Dequant4Args& a, hipStream_t st) {
+    const int chunks = (a.d + kChunk - 1) / kChunk, tx = across(chunks), ty = 256 / tx;
+    const int64_t cols = (chunks + tx - 1) / tx, most = (2048 + cols - 1) / cols;   // 8 workgroups a compute unit
+    int64_t rows_wg = (a.rows + most - 1) / most;
+    rows_wg = (rows_wg + ty - 1) / ty * ty;
+    const dim3 grid((unsigned)cols, (unsigned)((a.rows + rows_wg - 1) / rows_wg));
+    return launch_kernel(k_dequant4<BF, SCALE>, grid, 256, 0, st, a, tx, (int)rows_wg);
+}
+
+}  // namespace
+
+hipError_t launch_quant4(const Rows4Args& a, hipStream_t st) {
+    return a.x_bf16 ? launch_quant<true>(a, st) : launch_quant<false>(a, st);
+}
+
+hipError_t launch_rmsnorm4(const Rows4Args& a, hipStream_t st) {
+    if (a.x_bf16) return a.factor ? launch_norm<true, true>(a, st) : launch_norm<true, false>(a, st);
+    return a.factor ? launch_norm<false, true>(a, st) : launch_norm<false, false>(a, st);
+}
+
+hipError_t launch_dequant4(const Dequant4Args& a, hipStream_t st) {
+    if (a.scale) return a.out_bf16 ? launch_dequant<true, true>(a, st) : launch_dequant<false, true>(a, st);
+    return a.out_bf16 ? launch_dequant<true, false>(a, st) : launch_dequant<false, false>(a, st);
+}
+
+}  // namespace qamw
