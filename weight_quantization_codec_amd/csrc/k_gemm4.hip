@@ -27,102 +27,400 @@ __device__ __forceinline__ f32x16 mfma4(i32x4 w, i32x4 x, f32x16 acc, int sw, in
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x8, acc, kFp4, kFp4, B, sw, B, sx);
 }
 
-// Rows in groups: the expert and the rows of the tile `tile` of `bm` rows, counted over all groups; false past the
-// last tile.  Every lane of the wavefront calls this.
-__device__ __forceinline__ int clamped(const int32_t* offsets, int e, int rows) {
-    const int o = offsets[e];
-    return o < 0 ? 0 : o > rows ? rows : o;
-}
-__device__ __forceinline__ bool group_tile(const Gemm4Args& a, int bm, int tile, int& expert, int& first, int& end) {
-    const int lane = threadIdx.x % kWave;
-    for (int e0 = 0; e0 < a.experts; e0 += kWave) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < a.experts) {
-            lo = clamped(a.offsets, e, a.M);
-            hi = clamped(a.offsets, e + 1, a.M);
-        }
-        const int tiles = hi > lo ? (hi - lo + bm - 1) / bm : 0;
-        int sum = tiles;   // of this lane's groups and all before it
+// Rows in groups.  Tiles of `bm` rows are counted over all groups, each group beginning a tile of its own.  What the
+// groups are is known to the device only: a launch has workgroups for as many tiles as there may be, and those
+// without one leave.  Every wavefront counts by itself, 64 groups at a time, a group a lane.
+struct Groups {
+    int lo, hi, sum;   // the lane's group, held to the rows there are, and the tiles up to its end
+};
+__device__ __forceinline__ Groups groups_from(const Gemm4Args& a, int bm, int e) {
+    Groups g{0, 0, 0};
+    if (e < a.experts) {
+        const int lo = a.offsets[e], hi = a.offsets[e + 1];
+        g.lo = lo < 0 ? 0 : lo > a.M ? a.M : lo;
+        g.hi = hi < 0 ? 0 : hi > a.M ? a.M : hi;
+    }
+    g.sum = g.hi > g.lo ? (g.hi - g.lo + bm - 1) / bm : 0;
 #pragma unroll
-        for (int off = 1; off < kWave; off *= 2) {
-            const int below = __shfl_up(sum, off);
-            sum += lane >= off ? below : 0;
-        }
-        const uint64_t reached = __ballot(sum > tile);
+    for (int off = 1; off < kWave; off *= 2) {
+        const int below = __shfl_up(g.sum, off);
+        g.sum += (int)threadIdx.x % kWave >= off ? below : 0;
+    }
+    return g;
+}
+// The rows m0 .. m_end - 1 of workgroup b's tile, its expert and its tile of columns; false without one.
+__device__ __forceinline__ bool group_tile(const Gemm4Args& a, int bm, int b, int tiles_m, int tiles_n, int& expert,
+                                           int& m0, int& m_end, int& tile_n) {
+    const int lane = threadIdx.x % kWave;
+    Groups g{};
+    int total = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += kWave) {
+        g = groups_from(a, bm, e0 + lane);
+        total += __shfl(g.sum, kWave - 1);
+    }
+    total = total < tiles_m ? total : tiles_m;   // (more only where groups overlap)
+    if (b >= total * tiles_n) return false;
+    int tile;
+    tile_of(b, 1, total, tiles_n, tile, tile_n);
+    for (int e0 = 0;; e0 += kWave) {
+        if (a.experts > kWave) g = groups_from(a, bm, e0 + lane);
+        const uint64_t reached = __ballot(g.sum > tile);
         if (reached) {
             const int at = __builtin_ctzll(reached);
-            expert = e0 + at;
-            first = __shfl(lo, at) + (tile - __shfl(sum - tiles, at)) * bm;
-            end = __shfl(hi, at);
+            const int before = at > 0 ? __shfl(g.sum, at - 1) : 0;
+            expert = __builtin_amdgcn_readfirstlane(e0 + at);
+            m_end = __builtin_amdgcn_readfirstlane(__shfl(g.hi, at));
+            m0 = __builtin_amdgcn_readfirstlane(__shfl(g.lo, at) + (tile - before) * bm);
+            m_end = m_end < m0 + bm ? m_end : m0 + bm;
             return true;
         }
-        tile -= __shfl(sum, kWave - 1);
+        tile -= __shfl(g.sum, kWave - 1);
     }
-    return false;
 }
 
-// The simplest form: a wavefront has 32 rows of y and 32 columns, and loads its operands as they stand in memory.
-template <bool GROUPED>
-__device__ __forceinline__ void tile_simple(const Gemm4Args& a, int tile_m, int n0) {
-    const int lane = threadIdx.x % kWave, r = lane % 32, h = lane / 32;
-    int expert = 0, m0 = tile_m * 32, m_end = a.M;
-    if (GROUPED && !group_tile(a, 32, tile_m, expert, m0, m_end)) return;
-    const int n = n0 + r < a.N ? n0 + r : a.N - 1, m = m0 + r < m_end ? m0 + r : m_end - 1;
-    int row = m;
-    if (GROUPED && a.index) row = a.index[m];
-    const bool none = GROUPED && (row < 0 || row >= a.x_rows);
-    const uint8_t* x = a.xq + row * a.ld_x + h * 64;
-    const uint8_t* xe = a.xe + row * 8ll + h * 4;
-    const uint8_t* w = a.wq + (GROUPED ? expert * a.ld_wexpert : 0) + n * a.ld_w + h * 64;
-    const uint8_t* we = a.we + (GROUPED ? expert * a.ld_weexpert : 0) + n * 8ll + h * 4;
-    f32x16 acc = (f32x16)(0.0f);
-    for (int g = 0; g < a.groups; ++g) {
-        const int sx = none ? 0 : *reinterpret_cast<const int*>(xe + g * a.ld_xe);
-        const int sw = *reinterpret_cast<const int*>(we + g * a.ld_we);
-        static_for<4>([&](auto b) {
-            i32x4 fx = (i32x4)(0);
-            if (!none) fx = *reinterpret_cast<const i32x4*>(x + g * kGroupBytes + b * 16);
-            const i32x4 fw = *reinterpret_cast<const i32x4*>(w + g * kGroupBytes + b * 16);
-            acc = mfma4<b>(fw, fx, acc, sw, sx);
-        });
+// 4 bytes a lane from a buffer into LDS at lds + 4 lane, like load_lds16.
+__device__ __forceinline__ void load_lds4(u32x4 rsrc, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory");
+}
+
+// What a tile leaves: y, or its sums over a part of k, to be joined.
+enum { kF32 = 0, kBf16 = 1, kSums = 2 };
+
+// A tile of BM activation rows by BN weight rows, WM x 4 / WM wavefronts, S stages of a group of columns in LDS: the
+// rows' 128 bytes of codes, then their 8 bytes of scales.
+template <int BM, int BN, int WM, int S, int SP>
+struct TileCfg {
+    static constexpr int kWN = 4 / WM, kRowsM = BM / WM, kRowsN = BN / kWN;   // a wavefront's part
+    static constexpr int kTM = kRowsM / 32, kTN = kRowsN / 32;                // in blocks of 32 x 32
+    static constexpr int kCodeLoads = (BM + BN) / 32;        // loads of a wavefront and stage: 8 rows of codes each
+    static constexpr int kScaleRows = (BM + BN) / 32;        // 32 rows of scales each, for the workgroup
+    static constexpr int kScaleLoads = (kScaleRows + 3) / 4;
+    static constexpr int kLoads = kScaleLoads + kCodeLoads;
+    static constexpr int kCodes = (BM + BN) * kGroupBytes, kStage = kCodes + (BM + BN) * 8, kLds = S * kStage;
+    // A step has 4 sub-steps of two blocks a row.  During the first all operands of the step that are still in
+    // LDS are read; behind it the stage is free, and its refill is issued over SP matrix instructions.
+    static constexpr int kNS = 4, kMfma = kTM * kTN;
+    static constexpr int slot(int i) { return i * SP / kLoads; }
+    static constexpr int issued(int slots) {   // loads of a refill issued before the slot
+        int n = 0;
+        for (int i = 0; i < kLoads; ++i) n += slot(i) < slots;
+        return n;
     }
-    if (m0 + r >= m_end) return;
+};
+
+constexpr uint32_t kFar = 0xF0000000u;   // an offset past every buffer: what is loaded from there is 0
+
+template <int BM, int BN, int WM, int S, int SP, int OUT, bool GROUPED>
+__global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int tiles_n, int splits) {
+    using C = TileCfg<BM, BN, WM, S, SP>;
+    constexpr int TM = C::kTM, TN = C::kTN, NS = C::kNS;
+    // a refill ends before the next one begins; vmcnt counts to 63
+    static_assert(SP <= NS * C::kMfma && S * C::kLoads < 64 && S >= 2);
+    extern __shared__ __align__(1024) uint8_t lds[];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    int tile_m = 0, tile_n = 0, split = 0, expert = 0, m0 = 0, m_end = a.M;
+    if constexpr (GROUPED) {
+        if (!group_tile(a, BM, blockIdx.x, tiles_m, tiles_n, expert, m0, m_end, tile_n)) return;
+    } else {
+        split = tile_of(blockIdx.x, splits, tiles_m, tiles_n, tile_m, tile_n);
+        m0 = tile_m * BM;
+    }
+    const int n0 = tile_n * BN;
+    const int rows_m = m_end - m0 < BM ? m_end - m0 : BM, rows_n = a.N - n0 < BN ? a.N - n0 : BN;
+    // this workgroup's part of k: groups of columns first .. first + steps - 1
+    const int first = (int)((int64_t)a.groups * split / splits);
+    const int steps = (int)((int64_t)a.groups * (split + 1) / splits) - first;
+
+    // Loads.  One moves 8 rows of 128 bytes; LDS row r holds its 16-byte chunk c at place c ^ (r / 2 % 8).
+    // A 16-byte read goes through LDS in phases of 16 lanes over 64 banks, here 16 rows at one c: 8 even
+    // ones in one half of the banks and 8 odd ones in the other, each at a place of its own.
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    constexpr int kLoadsX = BM / 32;
+    const bool indexed = GROUPED && a.index;
+    // the row of x that row r of the tile is, and whether there is none
+    auto x_row = [&](int r, bool& none) {
+        const int row = a.index[m0 + (r < rows_m ? r : rows_m - 1)];
+        none = r >= rows_m || row < 0 || row >= a.x_rows;
+        return row;
+    };
+    uint32_t voff[C::kLoads];   // scales first
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int col = n0 + i / 4 * 8 + h * 4 + i % 4;
-        if (col >= a.N) continue;
-        const int64_t at = (int64_t)m * a.ld_y + col;
-        if (a.y_bf16)
-            reinterpret_cast<uint16_t*>(a.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)acc[i]);
+    for (int i = 0; i < C::kScaleLoads; ++i) {
+        const int at = i * 4 + wave, part = at < C::kScaleRows ? at : C::kScaleRows - 1;
+        const bool is_x = part < kLoadsX;
+        int row = (is_x ? part : part - kLoadsX) * 32 + lane / 2;
+        bool none = false;
+        if (indexed && is_x) row = x_row(row, none);
+        voff[i] = none ? kFar : (uint32_t)row * 8 + lane % 2 * 4;
+    }
+#pragma unroll
+    for (int i = 0; i < C::kCodeLoads; ++i) {
+        const bool is_x = i < kLoadsX;
+        const int r = ((is_x ? i : i - kLoadsX) * 4 + wave) * 8 + lane / 8;
+        int row = r;
+        bool none = false;
+        if (indexed && is_x) row = x_row(row, none);
+        voff[C::kScaleLoads + i] =
+            none ? kFar : (uint32_t)row * (uint32_t)(is_x ? a.ld_x : a.ld_w) + (uint32_t)((lane % 8) ^ (r / 2 % 8)) * 16;
+    }
+    const int64_t at_m = indexed ? 0 : m0;
+    const int64_t of_w = GROUPED ? expert * a.ld_wexpert : 0, of_we = GROUPED ? expert * a.ld_weexpert : 0;
+    const uint64_t base_x = (uint64_t)(a.xq + at_m * a.ld_x + (int64_t)first * kGroupBytes);
+    const uint64_t base_w = (uint64_t)(a.wq + of_w + n0 * a.ld_w + (int64_t)first * kGroupBytes);
+    const uint64_t base_xe = (uint64_t)(a.xe + at_m * 8 + first * a.ld_xe);
+    const uint64_t base_we = (uint64_t)(a.we + of_we + n0 * 8ll + first * a.ld_we);
+    // Buffers end with the last row that there is; a row's bytes behind this part of k are in them, and never read.
+    const int64_t have_x = indexed ? a.x_rows : rows_m;
+    const uint32_t left = (uint32_t)(a.groups - first) * kGroupBytes;
+    const uint32_t size_x = have_x ? (uint32_t)((have_x - 1) * a.ld_x) + left : 0;
+    const uint32_t size_w = (uint32_t)((rows_n - 1) * a.ld_w) + left;
+    // The buffers of step t, empty past the last step.  Loads past them touch no memory; the count of loads under
+    // way is the same in every step.
+    u32x4 rx, rw, rxe, rwe;
+    auto buffers = [&](int t) {
+        const bool in = t < steps;
+        rx = rsrc_of(base_x + (uint64_t)t * kGroupBytes, in && size_x ? size_x - (uint32_t)t * kGroupBytes : 0u);
+        rw = rsrc_of(base_w + (uint64_t)t * kGroupBytes, in ? size_w - (uint32_t)t * kGroupBytes : 0u);
+        rxe = rsrc_of(base_xe + t * a.ld_xe, in ? (uint32_t)have_x * 8 : 0u);
+        rwe = rsrc_of(base_we + t * a.ld_we, in ? (uint32_t)rows_n * 8 : 0u);
+        // a scalar register written by a vector instruction needs five wait states before a load reads it; the
+        // compiler does not look into the assembly of the loads
+        asm volatile("s_nop 4" ::"s"(rx), "s"(rw), "s"(rxe), "s"(rwe));
+    };
+    auto load = [&](int i, uint32_t stage) {
+        if (i < C::kScaleLoads) {
+            const int at = i * 4 + wave, part = at < C::kScaleRows ? at : C::kScaleRows - 1;
+            // (of the larger tiles, all four wavefronts load of the same operand)
+            const bool is_x = kLoadsX % 4 ? part < kLoadsX : i < kLoadsX / 4;
+            load_lds4(is_x ? rxe : rwe, voff[i], stage + C::kCodes + (uint32_t)part * 256);
+        } else {
+            const int j = i - C::kScaleLoads;
+            load_lds16(j < kLoadsX ? rx : rw, voff[i], stage + (uint32_t)(j * 4 + wave) * 1024);
+        }
+    };
+
+    // Operands: block row lane % 32, 16-byte chunk ks + 4 (lane / 32) of sub-step ks.
+    const int wm = wave / C::kWN, wn = wave % C::kWN;
+    uint32_t col[NS];
+#pragma unroll
+    for (int ks = 0; ks < NS; ++ks)
+        col[ks] = (lane % 32) * kGroupBytes + ((ks + lane / 32 * 4) ^ (lane / 2 % 8)) * 16;
+    const uint32_t row_x = wm * C::kRowsM * kGroupBytes, row_w = (BM + wn * C::kRowsN) * kGroupBytes;
+    const uint32_t scale_x = C::kCodes + (wm * C::kRowsM + lane % 32) * 8 + lane / 32 * 4;
+    const uint32_t scale_w = C::kCodes + (BM + wn * C::kRowsN + lane % 32) * 8 + lane / 32 * 4;
+    i32x4 fx[NS][TM], fw[NS][TN];
+    int sx[TM], sw[TN], next_sx[TM], next_sw[TN];
+    auto read = [&](int i, int set, const uint8_t* st, int ks) {
+        if (i < TN)
+            fw[set][i] = *reinterpret_cast<const i32x4*>(st + row_w + i * 32 * kGroupBytes + col[ks]);
         else
-            reinterpret_cast<float*>(a.y)[at] = acc[i];
+            fx[set][i - TN] = *reinterpret_cast<const i32x4*>(st + row_x + (i - TN) * 32 * kGroupBytes + col[ks]);
+    };
+    auto read_scale = [&](int i, const uint8_t* st) {
+        if (i < TN)
+            next_sw[i] = *reinterpret_cast<const int*>(st + scale_w + i * 256);
+        else
+            next_sx[i - TN] = *reinterpret_cast<const int*>(st + scale_x + (i - TN) * 256);
+    };
+    f32x16 acc[TN][TM];
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int m = 0; m < TM; ++m) acc[n][m] = (f32x16)(0.0f);
+
+    // The first S - 1 stages, and of the next one what a step issues before it ends.
+    constexpr int kRefillStart = (NS - 1) * C::kMfma;   // slots of a refill within its own step
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        buffers(s);
+#pragma unroll
+        for (int i = 0; i < (s < S - 1 ? C::kLoads : C::issued(kRefillStart)); ++i) load(i, lds0 + s * C::kStage);
+    }
+    wait_stage<(S - 2) * C::kLoads + C::issued(kRefillStart)>();
+    constexpr int kOps = TM + TN;
+#pragma unroll
+    for (int i = 0; i < kOps; ++i) read(i, 0, lds, 0), read_scale(i, lds);
+
+    int buf = 0, refill = S - 1;
+    for (int t = 0; t < steps; ++t) {
+        const int next = buf + 1 < S ? buf + 1 : 0;
+        const uint8_t* cur_p = lds + buf * C::kStage;
+        const uint8_t* next_p = lds + next * C::kStage;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) sw[i] = next_sw[i];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sx[i] = next_sx[i];
+        static_for<NS>([&](auto ks_) {
+            constexpr int ks = ks_;
+            if constexpr (ks == 1) {
+                // every wavefront has read this stage: its refill may begin
+                wait_reads();
+                buffers(t + S);
+                refill = buf;
+            } else if constexpr (ks == NS - 1) {
+                wait_stage<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma)>();
+            }
+            constexpr int reads = ks == 0 ? (NS - 1) * kOps : ks == NS - 1 ? kOps : 0;
+            static_for<C::kMfma>([&](auto j_) {
+                constexpr int j = j_;
+                static_for<reads>([&](auto i) {
+                    constexpr int at = reads > C::kMfma ? i * C::kMfma / reads : int(i), set = (ks + 1 + i / kOps) % NS;
+                    if constexpr (at == j) {
+                        read(i % kOps, set, ks == NS - 1 ? next_p : cur_p, set);
+                        if constexpr (ks == NS - 1) read_scale(i, next_p);
+                    }
+                });
+                constexpr int slot = ((ks + NS - 1) % NS) * C::kMfma + j;
+                static_for<C::kLoads>([&](auto i) {
+                    if constexpr (C::slot(i) == slot) load(i, lds0 + refill * C::kStage);
+                });
+                constexpr int n = j / TM, m = j % TM;
+                acc[n][m] = mfma4<ks>(fw[ks][n], fx[ks][m], acc[n][m], sw[n], sx[m]);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        });
+        buf = next;
+    }
+
+    // Rows of y through LDS, 32 at a time and wavefront, for stores of whole lines.  A lane has column
+    // m = lane % 32 of each block and rows n = 8 g + 4 (lane / 32) + 0..3.
+    wait_stage<0>();
+    constexpr int kEs = OUT == kBf16 ? 2 : 4, kRow = C::kRowsN * kEs, kChunks = kRow / 16;
+    constexpr int kParts = C::kLds / (4 * 32 * kRow) < TM ? C::kLds / (4 * 32 * kRow) : TM;
+    const int r = lane % 32, h = lane / 32;
+    const int64_t pitch = (OUT == kSums ? (int64_t)sums_pitch(a.N) : a.ld_y) * kEs;
+    const bool full = rows_m == BM && rows_n == BN;
+    uint8_t* out = reinterpret_cast<uint8_t*>(OUT == kSums ? a.work : a.y);
+    if (OUT == kSums) out += (int64_t)split * a.M * pitch;
+    uint8_t* y = out + ((int64_t)m0 + wm * C::kRowsM) * pitch + ((int64_t)n0 + wn * C::kRowsN) * kEs;
+    uint8_t* y_lane = y + (lane / kChunks) * pitch + (lane % kChunks) * 16;
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+        uint8_t* mine = lds + (m % kParts * 4 + wave) * 32 * kRow;
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int byte = (n * 32 + 8 * g + 4 * h) * kEs;
+                uint8_t* p = mine + r * kRow + (((byte / 16) ^ r) % kChunks) * 16 + byte % 16;
+                const float v[4] = {acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
+                if constexpr (OUT == kBf16)
+                    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+                else
+                    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        constexpr int kStores = 32 * kChunks / kWave, kRowsStore = kWave / kChunks;
+        const int c = lane % kChunks;
+        if (full) {
+#pragma unroll
+            for (int i = 0; i < kStores; ++i) {
+                const int row = i * kRowsStore + lane / kChunks;
+                *reinterpret_cast<Out16*>(y_lane + (m * 32 + i * kRowsStore) * pitch) =
+                    *reinterpret_cast<const Out16*>(mine + row * kRow + ((c ^ row) % kChunks) * 16);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < kStores; ++i) {
+                const int row = i * kRowsStore + lane / kChunks;
+                const int left_n = rows_n - wn * C::kRowsN - c * (16 / kEs);
+                const uint8_t* p = mine + row * kRow + ((c ^ row) % kChunks) * 16;
+                uint8_t* to = y_lane + (m * 32 + i * kRowsStore) * pitch;
+                if (wm * C::kRowsM + m * 32 + row >= rows_m || left_n <= 0) continue;
+                if (left_n >= 16 / kEs) {
+                    *reinterpret_cast<Out16*>(to) = *reinterpret_cast<const Out16*>(p);
+                } else {
+                    for (int e = 0; e < left_n; ++e) {
+                        if constexpr (OUT == kBf16)
+                            reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(p)[e];
+                        else
+                            reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(p)[e];
+                    }
+                }
+            }
+        }
     }
 }
 
-template <bool GROUPED>
-__global__ __launch_bounds__(256) void k_gemm4_simple(Gemm4Args a, int tiles_m) {
-    const int tiles_n = (a.N + 31) / 32;
-    const int64_t all = (int64_t)tiles_m * tiles_n;
-    for (int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; t < all; t += (int64_t)gridDim.x * 4)
-        tile_simple<GROUPED>(a, (int)(t / tiles_n), (int)(t % tiles_n) * 32);
+// Adds the sums of the parts of k, in their order: 4 columns of a row a thread.
+template <bool BF>
+__global__ __launch_bounds__(256) void k_gemm4_join(Gemm4Args a, int splits) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    const int pitch = sums_pitch(a.N), quads = (a.N + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = i / quads;
+    const int n = (int)(i % quads) * 4;
+    if (m >= a.M) return;
+    const float* p = reinterpret_cast<const float*>(a.work) + m * pitch + n;
+    f32x4 c = *reinterpret_cast<const f32x4*>(p);
+    int s = 1;
+    for (; s + 3 <= splits; s += 3) {   // three loads under way at a time
+        f32x4 v[3];
+#pragma unroll
+        for (int u = 0; u < 3; ++u) v[u] = *reinterpret_cast<const f32x4*>(p + (int64_t)(s + u) * a.M * pitch);
+#pragma unroll
+        for (int u = 0; u < 3; ++u) c += v[u];
+    }
+    for (; s < splits; ++s) c += *reinterpret_cast<const f32x4*>(p + (int64_t)s * a.M * pitch);
+    if constexpr (BF) {
+        uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + m * a.ld_y + n;
+        const Out8 o = {{bf16_pair(c[0], c[1]), bf16_pair(c[2], c[3])}};
+        if (n + 4 <= a.N)
+            *reinterpret_cast<Out8*>(y) = o;
+        else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (n + e < a.N) y[e] = (uint16_t)(o.w[e / 2] >> (16 * (e % 2)));
+        }
+    } else {
+        float* y = reinterpret_cast<float*>(a.y) + m * a.ld_y + n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) y[e] = c[e];
+    }
 }
 
-template <bool GROUPED>
-hipError_t launch_simple(const Gemm4Args& a, int tiles_m, hipStream_t st) {
-    const int64_t wgs = ((int64_t)tiles_m * ((a.N + 31) / 32) + 3) / 4, most = 1 << 20;
-    return launch_kernel(k_gemm4_simple<GROUPED>, dim3((unsigned)(wgs < most ? wgs : most)), 256, 0, st, a, tiles_m);
+template <int BM, int BN, int WM, int S, int SP, int OUT, bool GROUPED>
+hipError_t launch_tile_kernel(const Gemm4Args& a, int tiles_m, int tiles_n, int splits, hipStream_t st) {
+    using C = TileCfg<BM, BN, WM, S, SP>;
+    auto kernel = k_gemm4<BM, BN, WM, S, SP, OUT, GROUPED>;
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_big_lds(kernel, C::kLds, done);
+    if (e != hipSuccess) return e;
+    return launch_kernel(kernel, dim3((unsigned)(tiles_m * tiles_n * splits)), 256, C::kLds, st, a, tiles_m, tiles_n,
+                         splits);
+}
+
+template <int BM, int BN, int WM, int S, int SP>
+hipError_t launch_tiles(const Gemm4Args& a, int splits, hipStream_t st) {
+    const int tiles_m = (int)(((int64_t)a.M + BM - 1) / BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
+    if (splits == 1)
+        return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, kBf16, false>(a, tiles_m, tiles_n, 1, st)
+                        : launch_tile_kernel<BM, BN, WM, S, SP, kF32, false>(a, tiles_m, tiles_n, 1, st);
+    const hipError_t e = launch_tile_kernel<BM, BN, WM, S, SP, kSums, false>(a, tiles_m, tiles_n, splits, st);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)(((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256));
+    return launch_kernel(a.y_bf16 ? k_gemm4_join<true> : k_gemm4_join<false>, grid, 256, 0, st, a, splits);
+}
+
+// Tiles of rows that `rows` rows in `experts` groups can need: every group's last one may be a part of one.
+int group_tiles(int rows, int experts, int bm) { return rows / bm + (experts < rows ? experts : rows); }
+
+template <int BM, int BN, int WM, int S, int SP>
+hipError_t launch_group_tiles(const Gemm4Args& a, hipStream_t st) {
+    const int tiles_m = group_tiles(a.M, a.experts, BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
+    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, kBf16, true>(a, tiles_m, tiles_n, 1, st)
+                    : launch_tile_kernel<BM, BN, WM, S, SP, kF32, true>(a, tiles_m, tiles_n, 1, st);
 }
 
 }  // namespace
 
 size_t gemm4_workspace(int, int, int) { return 0; }
 
-hipError_t launch_gemm4(const Gemm4Args& a, hipStream_t st) { return launch_simple<false>(a, (a.M + 31) / 32, st); }
+hipError_t launch_gemm4(const Gemm4Args& a, hipStream_t st) { return launch_tiles<256, 256, 2, 2, 48>(a, 1, st); }
 
-hipError_t launch_gemm4_grouped(const Gemm4Args& a, hipStream_t st) {
-    // every group's last tile may be a part of one
-    return launch_simple<true>(a, a.M / 32 + (a.experts < a.M ? a.experts : a.M), st);
-}
+hipError_t launch_gemm4_grouped(const Gemm4Args& a, hipStream_t st) { return launch_group_tiles<256, 256, 2, 2, 48>(a, st); }
 
 }  // namespace qamw
