@@ -131,9 +131,10 @@ int qamw_gemm4(const uint8_t* d_xq, int64_t ld_x, const uint8_t* d_xe, int64_t l
  *                that more than one has, and any behind the first overlap, are unspecified.
  *   d_y, y_dtype, ld_y  rows x d_out, ld_y >= d_out; it overlaps no input.
  * Limits of qamw_gemm4 for rows, x_rows, d_out, groups and leading dimensions; 1 <= experts <=
- * QAMW_GEMM4_MAX_EXPERTS, and with d_index x_rows * ld_x <= QAMW_GEMM4_MAX_INDEXED bytes (QAMW_ERR_UNSUPPORTED above).
- * rows = 0 or d_out = 0 is a no-op. */
+ * QAMW_GEMM4_MAX_EXPERTS, experts * d_out <= QAMW_GEMM4_MAX_EXPERT_ROWS, and with d_index x_rows * ld_x <=
+ * QAMW_GEMM4_MAX_INDEXED bytes (QAMW_ERR_UNSUPPORTED above).  rows = 0 or d_out = 0 is a no-op. */
 #define QAMW_GEMM4_MAX_EXPERTS 1024
+#define QAMW_GEMM4_MAX_EXPERT_ROWS (1 << 30)
 #define QAMW_GEMM4_MAX_INDEXED (1ll << 31)
 int qamw_gemm4_grouped(const uint8_t* d_xq, int64_t ld_x, const uint8_t* d_xe, int64_t ld_xe, int32_t x_rows,
                        const int32_t* d_index, int32_t rows, const uint8_t* d_wq, int64_t ld_w, int64_t ld_wexpert,

@@ -51,7 +51,7 @@ def test_stride_and_groups(lib):
 def test_header_limits_match_binding():
     text = open(q.MX4_HEADER_PATH).read()
     for name in ("MX4_MAX_NORM_COLS", "MX4_MAX_COLS", "GEMM4_MAX_ROWS", "GEMM4_MAX_LD", "GEMM4_MAX_OUT",
-                 "GEMM4_MAX_EXPERTS", "GEMM4_MAX_INDEXED"):
+                 "GEMM4_MAX_EXPERTS", "GEMM4_MAX_EXPERT_ROWS", "GEMM4_MAX_INDEXED"):
         m = re.search(r"#define QAMW_%s (.*)" % name, text)
         assert m and eval(m.group(1).replace("ll", "")) == getattr(q.mx4, name), name
 
@@ -167,6 +167,7 @@ def _grouped(lib, **kw):
     (dict(rows=(1 << 24) + 1, index=FAKE), UNSUP), (dict(x_rows=(1 << 24) + 1, ld_xe=1 << 28), UNSUP),
     (dict(by=-16), ARG), (dict(by=8), ARG), (dict(eby=-8), ARG), (dict(eby=4), ARG), (dict(off=None), ARG),
     (dict(off=FAKE + 2), ARG), (dict(index=FAKE + 2), ARG),
+    (dict(E=1024, N=(1 << 20) + 1, ld_y=1 << 21, ld_we=1 << 24), UNSUP),   # 2^30 rows of weights and more
     (dict(index=FAKE, x_rows=1 << 24, ld_xe=1 << 27), UNSUP),   # 2^32 bytes of codes to choose rows from
 ])
 def test_gemm4_grouped_rejects(lib, kw, code):

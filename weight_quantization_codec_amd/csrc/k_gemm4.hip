@@ -7,6 +7,7 @@
 // the four bytes of a register, from which the instruction takes the one that it is told.
 #include "qamw_device.hpp"
 #include "qamw_mx4_launch.hpp"
+#include "qamw_mx4_plan.hpp"
 #include "qamw_rows.hpp"
 #include "qamw_tile.hpp"
 
@@ -91,7 +92,7 @@ enum { kF32 = 0, kBf16 = 1, kSums = 2 };
 
 // A tile of BM activation rows by BN weight rows, WM x 4 / WM wavefronts, S stages of a group of columns in LDS: the
 // rows' 128 bytes of codes, then their 8 bytes of scales.
-template <int BM, int BN, int WM, int S, int SP>
+template <int BM, int BN, int WM, int S, int SP, int FA>
 struct TileCfg {
     static constexpr int kWN = 4 / WM, kRowsM = BM / WM, kRowsN = BN / kWN;   // a wavefront's part
     static constexpr int kTM = kRowsM / 32, kTN = kRowsN / 32;                // in blocks of 32 x 32
@@ -100,7 +101,7 @@ struct TileCfg {
     static constexpr int kScaleLoads = (kScaleRows + 3) / 4;
     static constexpr int kLoads = kScaleLoads + kCodeLoads;
     static constexpr int kCodes = (BM + BN) * kGroupBytes, kStage = kCodes + (BM + BN) * 8, kLds = S * kStage;
-    // A step has 4 sub-steps of two blocks a row.  During the first all operands of the step that are still in
+    // A step has 4 sub-steps of two blocks a row.  During sub-step FA all operands of the step that are still in
     // LDS are read; behind it the stage is free, and its refill is issued over SP matrix instructions.
     static constexpr int kNS = 4, kMfma = kTM * kTN;
     static constexpr int slot(int i) { return i * SP / kLoads; }
@@ -113,9 +114,9 @@ struct TileCfg {
 
 constexpr uint32_t kFar = 0xF0000000u;   // an offset past every buffer: what is loaded from there is 0
 
-template <int BM, int BN, int WM, int S, int SP, int OUT, bool GROUPED>
+template <int BM, int BN, int WM, int S, int SP, int FA, int OUT, bool GROUPED>
 __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int tiles_n, int splits) {
-    using C = TileCfg<BM, BN, WM, S, SP>;
+    using C = TileCfg<BM, BN, WM, S, SP, FA>;
     constexpr int TM = C::kTM, TN = C::kTN, NS = C::kNS;
     // a refill ends before the next one begins; vmcnt counts to 63
     static_assert(SP <= NS * C::kMfma && S * C::kLoads < 64 && S >= 2);
@@ -131,8 +132,9 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     const int n0 = tile_n * BN;
     const int rows_m = m_end - m0 < BM ? m_end - m0 : BM, rows_n = a.N - n0 < BN ? a.N - n0 : BN;
     // this workgroup's part of k: groups of columns first .. first + steps - 1
-    const int first = (int)((int64_t)a.groups * split / splits);
-    const int steps = (int)((int64_t)a.groups * (split + 1) / splits) - first;
+    // (at most 2^15 groups in 16 parts: 32 bits do, and a division of 64 bits takes a thousand cycles)
+    const int first = (int)((uint32_t)(a.groups * split) / (uint32_t)splits);
+    const int steps = (int)((uint32_t)(a.groups * (split + 1)) / (uint32_t)splits) - first;
 
     // Loads.  One moves 8 rows of 128 bytes; LDS row r holds its 16-byte chunk c at place c ^ (r / 2 % 8).
     // A 16-byte read goes through LDS in phases of 16 lanes over 64 banks, here 16 rows at one c: 8 even
@@ -225,20 +227,23 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
         else
             next_sx[i - TN] = *reinterpret_cast<const int*>(st + scale_x + (i - TN) * 256);
     };
-    f32x16 acc[TN][TM];
-#pragma unroll
-    for (int n = 0; n < TN; ++n)
-#pragma unroll
-        for (int m = 0; m < TM; ++m) acc[n][m] = (f32x16)(0.0f);
 
     // The first S - 1 stages, and of the next one what a step issues before it ends.
-    constexpr int kRefillStart = (NS - 1) * C::kMfma;   // slots of a refill within its own step
+    constexpr int kRefillStart = (NS - 1 - FA) * C::kMfma;   // slots of a refill within its own step
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         buffers(s);
 #pragma unroll
         for (int i = 0; i < (s < S - 1 ? C::kLoads : C::issued(kRefillStart)); ++i) load(i, lds0 + s * C::kStage);
     }
+    f32x16 acc[TN][TM];   // zeroed while the first loads are under way
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int m = 0; m < TM; ++m) {
+            acc[n][m] = (f32x16)(0.0f);
+            asm volatile("" : "+a"(acc[n][m]));
+        }
     wait_stage<(S - 2) * C::kLoads + C::issued(kRefillStart)>();
     constexpr int kOps = TM + TN;
 #pragma unroll
@@ -255,15 +260,16 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
         for (int i = 0; i < TM; ++i) sx[i] = next_sx[i];
         static_for<NS>([&](auto ks_) {
             constexpr int ks = ks_;
-            if constexpr (ks == 1) {
+            if constexpr (ks == FA + 1) {
                 // every wavefront has read this stage: its refill may begin
-                wait_reads();
+                if constexpr (ks < NS - 1) wait_reads();
+                else wait_stage<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma)>();
                 buffers(t + S);
                 refill = buf;
             } else if constexpr (ks == NS - 1) {
                 wait_stage<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma)>();
             }
-            constexpr int reads = ks == 0 ? (NS - 1) * kOps : ks == NS - 1 ? kOps : 0;
+            constexpr int reads = ks < FA || ks == NS - 1 ? kOps : ks == FA ? (NS - 1 - FA) * kOps : 0;
             static_for<C::kMfma>([&](auto j_) {
                 constexpr int j = j_;
                 static_for<reads>([&](auto i) {
@@ -273,7 +279,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
                         if constexpr (ks == NS - 1) read_scale(i, next_p);
                     }
                 });
-                constexpr int slot = ((ks + NS - 1) % NS) * C::kMfma + j;
+                constexpr int slot = ((ks + NS - 1 - FA) % NS) * C::kMfma + j;
                 static_for<C::kLoads>([&](auto i) {
                     if constexpr (C::slot(i) == slot) load(i, lds0 + refill * C::kStage);
                 });
@@ -382,10 +388,10 @@ __global__ __launch_bounds__(256) void k_gemm4_join(Gemm4Args a, int splits) {
     }
 }
 
-template <int BM, int BN, int WM, int S, int SP, int OUT, bool GROUPED>
+template <int BM, int BN, int WM, int S, int SP, int FA, int OUT, bool GROUPED>
 hipError_t launch_tile_kernel(const Gemm4Args& a, int tiles_m, int tiles_n, int splits, hipStream_t st) {
-    using C = TileCfg<BM, BN, WM, S, SP>;
-    auto kernel = k_gemm4<BM, BN, WM, S, SP, OUT, GROUPED>;
+    using C = TileCfg<BM, BN, WM, S, SP, FA>;
+    auto kernel = k_gemm4<BM, BN, WM, S, SP, FA, OUT, GROUPED>;
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_big_lds(kernel, C::kLds, done);
     if (e != hipSuccess) return e;
@@ -393,34 +399,217 @@ hipError_t launch_tile_kernel(const Gemm4Args& a, int tiles_m, int tiles_n, int 
                          splits);
 }
 
-template <int BM, int BN, int WM, int S, int SP>
+template <int BM, int BN, int WM, int S, int SP, int FA>
 hipError_t launch_tiles(const Gemm4Args& a, int splits, hipStream_t st) {
     const int tiles_m = (int)(((int64_t)a.M + BM - 1) / BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
     if (splits == 1)
-        return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, kBf16, false>(a, tiles_m, tiles_n, 1, st)
-                        : launch_tile_kernel<BM, BN, WM, S, SP, kF32, false>(a, tiles_m, tiles_n, 1, st);
-    const hipError_t e = launch_tile_kernel<BM, BN, WM, S, SP, kSums, false>(a, tiles_m, tiles_n, splits, st);
+        return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, FA, kBf16, false>(a, tiles_m, tiles_n, 1, st)
+                        : launch_tile_kernel<BM, BN, WM, S, SP, FA, kF32, false>(a, tiles_m, tiles_n, 1, st);
+    const hipError_t e = launch_tile_kernel<BM, BN, WM, S, SP, FA, kSums, false>(a, tiles_m, tiles_n, splits, st);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)(((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256));
     return launch_kernel(a.y_bf16 ? k_gemm4_join<true> : k_gemm4_join<false>, grid, 256, 0, st, a, splits);
 }
 
-// Tiles of rows that `rows` rows in `experts` groups can need: every group's last one may be a part of one.
-int group_tiles(int rows, int experts, int bm) { return rows / bm + (experts < rows ? experts : rows); }
-
-template <int BM, int BN, int WM, int S, int SP>
+template <int BM, int BN, int WM, int S, int SP, int FA>
 hipError_t launch_group_tiles(const Gemm4Args& a, hipStream_t st) {
-    const int tiles_m = group_tiles(a.M, a.experts, BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
-    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, kBf16, true>(a, tiles_m, tiles_n, 1, st)
-                    : launch_tile_kernel<BM, BN, WM, S, SP, kF32, true>(a, tiles_m, tiles_n, 1, st);
+    const int tiles_m = (int)group_tiles(a.M, a.experts, BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
+    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, FA, kBf16, true>(a, tiles_m, tiles_n, 1, st)
+                    : launch_tile_kernel<BM, BN, WM, S, SP, FA, kF32, true>(a, tiles_m, tiles_n, 1, st);
+}
+
+// Few activation rows: bound by the one read of the weights.  A workgroup has up to 32 weight rows and W wavefronts
+// that split k between them.  Each wavefront runs on its own: it loads a group of columns of all rows (a unit) at a
+// time into its own ring of S units in LDS (XL loads of 8 activation rows, 4 of weight rows, and their scales), and
+// waits for nothing but its own loads.
+template <int W, int S, int XL>
+struct ThinCfg {
+    static constexpr int kMT = XL > 4 ? 2 : 1, kXScales = (XL + 3) / 4;   // blocks and scale loads of activation rows
+    static constexpr int kLoads = 5 + XL + kXScales;
+    static constexpr int kAtX = 4096 + 256, kAtXScales = kAtX + XL * 1024, kUnit = kAtXScales + kXScales * 256;
+    static constexpr int kRing = W * S * kUnit, kPart = W * kMT * 4096, kLds = kRing > kPart ? kRing : kPart;
+};
+
+template <int W, int S, int XL, int OUT, bool GROUPED>
+__global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows, int tiles_m, int tiles_n) {
+    using C = ThinCfg<W, S, XL>;
+    constexpr int MT = C::kMT, kLoads = C::kLoads, kUnit = C::kUnit;
+    static_assert(S * kLoads < 64);   // vmcnt counts to 63
+    extern __shared__ __align__(1024) uint8_t lds[];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    int tile_n = blockIdx.x, expert = 0, m0 = 0, m_end = a.M;
+    if constexpr (GROUPED) {
+        if (!group_tile(a, XL * 8, blockIdx.x, tiles_m, tiles_n, expert, m0, m_end, tile_n)) return;
+    }
+    const int n0 = tile_n * rows, rows_n = a.N - n0 < rows ? a.N - n0 : rows, rows_m = m_end - m0;
+    const int u0 = a.groups * wave / W, u1 = a.groups * (wave + 1) / W;
+    const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds + wave * S * kUnit;
+    const uint8_t* ring_p = lds + wave * S * kUnit;
+    const bool indexed = GROUPED && a.index;
+    auto x_row = [&](int r, bool& none) {
+        const int row = a.index[m0 + (r < rows_m ? r : rows_m - 1)];
+        none = r >= rows_m || row < 0 || row >= a.x_rows;
+        return row;
+    };
+    uint32_t voff_w[4], voff_x[XL], voff_we, voff_xe[C::kXScales];   // the layout of a stage of a tile
+    voff_we = (uint32_t)lane * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 8;
+        voff_w[i] = (uint32_t)r * (uint32_t)a.ld_w + (uint32_t)((lane % 8) ^ (r / 2 % 8)) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+        const int r = i * 8 + lane / 8;
+        int row = r;
+        bool none = false;
+        if (indexed) row = x_row(row, none);
+        voff_x[i] = none ? kFar : (uint32_t)row * (uint32_t)a.ld_x + (uint32_t)((lane % 8) ^ (r / 2 % 8)) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < C::kXScales; ++i) {
+        int row = i * 32 + lane / 2;
+        bool none = false;
+        if (indexed) row = x_row(row, none);
+        voff_xe[i] = none ? kFar : (uint32_t)row * 8 + lane % 2 * 4;
+    }
+    const int64_t at_m = indexed ? 0 : m0;
+    const uint64_t base_x = (uint64_t)(a.xq + at_m * a.ld_x), base_xe = (uint64_t)(a.xe + at_m * 8);
+    const uint64_t base_w = (uint64_t)(a.wq + (GROUPED ? expert * a.ld_wexpert : 0) + n0 * a.ld_w);
+    const uint64_t base_we = (uint64_t)(a.we + (GROUPED ? expert * a.ld_weexpert : 0) + n0 * 8ll);
+    const int64_t have_x = indexed ? a.x_rows : rows_m;
+    const uint32_t stride = (uint32_t)a.groups * kGroupBytes;
+    const uint32_t size_x = have_x ? (uint32_t)((have_x - 1) * a.ld_x) + stride : 0;
+    const uint32_t size_w = (uint32_t)((rows_n - 1) * a.ld_w) + stride;
+    auto load = [&](int u, int slot) {   // past the wavefront's part: from empty buffers
+        const bool in = u < u1;
+        const uint32_t at = (uint32_t)u * kGroupBytes;
+        const u32x4 rw = rsrc_of(base_w + at, in ? size_w - at : 0);
+        const u32x4 rx = rsrc_of(base_x + at, in && size_x ? size_x - at : 0);
+        const u32x4 rwe = rsrc_of(base_we + u * a.ld_we, in ? (uint32_t)rows_n * 8 : 0);
+        const u32x4 rxe = rsrc_of(base_xe + u * a.ld_xe, in ? (uint32_t)have_x * 8 : 0);
+        asm volatile("s_nop 4" ::"s"(rw), "s"(rx), "s"(rwe), "s"(rxe));
+        const uint32_t to = ring + slot * kUnit;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_lds16(rw, voff_w[i], to + i * 1024);
+        load_lds4(rwe, voff_we, to + 4096);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) load_lds16(rx, voff_x[i], to + C::kAtX + i * 1024);
+#pragma unroll
+        for (int i = 0; i < C::kXScales; ++i) load_lds4(rxe, voff_xe[i], to + C::kAtXScales + i * 256);
+    };
+#pragma unroll
+    for (int s = 0; s < S; ++s) load(u0 + s, s);
+    // with fewer than 32 rows of activations in the ring, columns past them repeat its first rows
+    constexpr int kWrap = XL < 4 ? XL * 8 : 32;
+    uint32_t col_w[4], col_x[4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+        const int r = lane % kWrap;
+        col_w[ks] = (lane % 32) * kGroupBytes + ((ks + lane / 32 * 4) ^ (lane / 2 % 8)) * 16;
+        col_x[ks] = r * kGroupBytes + ((ks + lane / 32 * 4) ^ (r / 2 % 8)) * 16;
+    }
+    const uint32_t at_we = 4096 + lane % 32 * 8 + lane / 32 * 4;
+    const uint32_t at_xe = C::kAtXScales + lane % kWrap * 8 + lane / 32 * 4;
+    f32x16 acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = (f32x16)(0.0f);
+    int slot = 0;
+    for (int u = u0; u < u1; ++u) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * kLoads) : "memory");
+        const uint8_t* p = ring_p + slot * kUnit;
+        i32x4 fw[4], fx[4][MT];
+        int sx[MT];
+        const int sw = *reinterpret_cast<const int*>(p + at_we);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) sx[m] = *reinterpret_cast<const int*>(p + at_xe + m * 256);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            fw[ks] = *reinterpret_cast<const i32x4*>(p + col_w[ks]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                fx[ks][m] = *reinterpret_cast<const i32x4*>(p + C::kAtX + m * 4096 + col_x[ks]);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot is read: refill it
+        load(u + S, slot);
+        static_for<4>([&](auto ks) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m] = mfma4<ks>(fw[ks], fx[ks][m], acc[m], sw, sx[m]);
+        });
+        slot = slot + 1 < S ? slot + 1 : 0;
+    }
+    wait_stage<0>();
+    float* part = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[((wave * MT + m) * 16 + i) * kWave + lane] = acc[m][i];
+    __syncthreads();
+    const int most = rows_m < XL * 8 ? rows_m : XL * 8;
+    for (int o = threadIdx.x; o < most * 32; o += W * kWave) {
+        const int m = o / 32, n = o % 32;
+        if (n >= rows_n) continue;
+        const float* p = part + (m / 32 * 16 + n / 8 * 4 + n % 4) * kWave + n / 4 % 2 * 32 + m % 32;
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) y += p[w * MT * 16 * kWave];
+        const int64_t at = (int64_t)(m0 + m) * a.ld_y + n0 + n;
+        if constexpr (OUT == kBf16)
+            reinterpret_cast<uint16_t*>(a.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)y);
+        else
+            reinterpret_cast<float*>(a.y)[at] = y;
+    }
+}
+
+template <int W, int S, int XL, int OUT, bool GROUPED>
+hipError_t launch_thin_kernel(const Gemm4Args& a, int rows, hipStream_t st) {
+    using C = ThinCfg<W, S, XL>;
+    const int tiles_n = (a.N + rows - 1) / rows, tiles_m = GROUPED ? (int)group_tiles(a.M, a.experts, XL * 8) : 1;
+    auto kernel = k_gemm4_thin<W, S, XL, OUT, GROUPED>;
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_big_lds(kernel, C::kLds, done);
+    if (e != hipSuccess) return e;
+    return launch_kernel(kernel, dim3((unsigned)(tiles_n * tiles_m)), W * kWave, C::kLds, st, a, rows, tiles_m, tiles_n);
+}
+
+template <int OUT>
+hipError_t launch_thin(const Gemm4Args& a, hipStream_t st) {
+    const int rows = thin_rows(a.N);
+    if (a.M <= 8) return launch_thin_kernel<4, 2, 1, OUT, false>(a, rows, st);
+    if (a.M <= 16) return launch_thin_kernel<4, 2, 2, OUT, false>(a, rows, st);
+    return launch_thin_kernel<4, 2, 4, OUT, false>(a, rows, st);
 }
 
 }  // namespace
 
-size_t gemm4_workspace(int, int, int) { return 0; }
+size_t gemm4_workspace(int M, int N, int groups) {
+    if (M == 0 || N == 0) return 0;
+    const Plan4 p = plan4(M, N, groups);
+    return p.splits > 1 ? (size_t)p.splits * M * sums_pitch(N) * 4 : 0;
+}
 
-hipError_t launch_gemm4(const Gemm4Args& a, hipStream_t st) { return launch_tiles<256, 256, 2, 2, 48>(a, 1, st); }
+hipError_t launch_gemm4(const Gemm4Args& a, hipStream_t st) {
+    const Plan4 p = plan4(a.M, a.N, a.groups);
+    switch (p.tile) {
+    case 0: return launch_tiles<256, 256, 2, 2, 48, 0>(a, p.splits, st);
+    case 1: return launch_tiles<128, 256, 2, 3, 32, 0>(a, p.splits, st);
+    case 2: return launch_tiles<128, 128, 2, 4, 16, 0>(a, p.splits, st);
+    case 3: return launch_tiles<64, 256, 1, 3, 16, 0>(a, p.splits, st);
+    case 4: return launch_tiles<32, 256, 1, 4, 8, 0>(a, p.splits, st);
+    case 5: return launch_tiles<64, 64, 2, 8, 4, 0>(a, p.splits, st);
+    default: return a.y_bf16 ? launch_thin<kBf16>(a, st) : launch_thin<kF32>(a, st);
+    }
+}
 
-hipError_t launch_gemm4_grouped(const Gemm4Args& a, hipStream_t st) { return launch_group_tiles<256, 256, 2, 2, 48>(a, st); }
+hipError_t launch_gemm4_grouped(const Gemm4Args& a, hipStream_t st) {
+    switch (plan4_grouped(a.M, a.experts, a.N)) {
+    case 0: return launch_group_tiles<256, 256, 2, 2, 48, 0>(a, st);
+    case 1: return launch_group_tiles<128, 256, 2, 3, 32, 0>(a, st);
+    case 3: return launch_group_tiles<64, 256, 1, 3, 16, 0>(a, st);
+    case 4: return launch_group_tiles<32, 256, 1, 4, 8, 0>(a, st);
+    default: return a.y_bf16 ? launch_thin_kernel<4, 2, 1, kBf16, true>(a, 32, st)
+                             : launch_thin_kernel<4, 2, 1, kF32, true>(a, 32, st);
+    }
+}
 
 }  // namespace qamw

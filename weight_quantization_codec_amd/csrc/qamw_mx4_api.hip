@@ -178,7 +178,8 @@ int qamw_gemm4_grouped(const uint8_t* d_xq, int64_t ld_x, const uint8_t* d_xe, i
     if (!is_dtype(y_dtype) || rows < 0 || x_rows < 0 || d_out < 0 || groups < 1 || experts < 1 || ld_y < d_out)
         return QAMW_ERR_ARG;
     if (!gemm4_fits(rows, d_out, groups) || x_rows > QAMW_GEMM4_MAX_ROWS || ld_x > QAMW_GEMM4_MAX_LD ||
-        ld_w > QAMW_GEMM4_MAX_LD || experts > QAMW_GEMM4_MAX_EXPERTS)
+        ld_w > QAMW_GEMM4_MAX_LD || experts > QAMW_GEMM4_MAX_EXPERTS ||
+        (int64_t)experts * d_out > QAMW_GEMM4_MAX_EXPERT_ROWS)
         return QAMW_ERR_UNSUPPORTED;
     if (d_index ? !aligned(d_index, 4) : x_rows < rows) return QAMW_ERR_ARG;
     if (rows == 0 || d_out == 0) return QAMW_OK;

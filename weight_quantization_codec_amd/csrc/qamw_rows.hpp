@@ -19,9 +19,12 @@ struct __attribute__((packed, aligned(4))) Float8 {
     float v[8];
 };
 
+// Two values as bf16, rounded to nearest even, by one v_cvt_pk_bf16_f32 (converted one by one, a pair takes four
+// instructions).
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    const uint32_t a = __builtin_bit_cast(uint16_t, (__bf16)lo), b = __builtin_bit_cast(uint16_t, (__bf16)hi);
-    return a | (b << 16);   // v_cvt_pk_bf16_f32: round to nearest even
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
 // The 8 columns of a chunk as they are stored, at any alignment of the elements.

@@ -43,6 +43,7 @@ GEMM4_MAX_ROWS = 1 << 24
 GEMM4_MAX_LD = 1 << 22
 GEMM4_MAX_OUT = 1 << 38
 GEMM4_MAX_EXPERTS = 1024
+GEMM4_MAX_EXPERT_ROWS = 1 << 30
 GEMM4_MAX_INDEXED = 1 << 31
 
 
