@@ -98,6 +98,7 @@ def load(path: Optional[str] = None):
     if path is None:
         _lib = lib
         _w8.bind(lib)
+        _mx4.bind(lib)
     return lib
 
 

@@ -53,17 +53,17 @@ def build(jobs: int = 8) -> str:
 
 
 def build_host() -> str:
-    """Compile the binding's host module (csrc/w8_host.cpp) against the installed torch.  Where that fails no older
-    module stays: w8.py does without one."""
+    """Compile the binding's host module (csrc/w8_host.cpp, mx4_host.cpp) against the installed torch.  Where that fails
+    no older module stays: w8.py and mx4.py do without one."""
     import sysconfig
 
     from torch.utils import cpp_extension
     tmp = HOST + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE, "-I", CSRC, "-I", sysconfig.get_paths()["include"]]
     for d in cpp_extension.include_paths("cuda"):
         cmd += ["-isystem", d]
-    cmd += [os.path.join(CSRC, "w8_host.cpp"), "-o", tmp]
+    cmd += [os.path.join(CSRC, "w8_host.cpp"), os.path.join(CSRC, "mx4_host.cpp"), "-o", tmp]
     for d in cpp_extension.library_paths():
         cmd += ["-L", d]
     cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
@@ -75,7 +75,7 @@ def build_host() -> str:
     if failure is not None:
         if os.path.exists(HOST):
             os.remove(HOST)
-        raise RuntimeError("g++ failed for w8_host.cpp:\n%s\n%s" % (" ".join(cmd), failure))
+        raise RuntimeError("g++ failed for w8_host.cpp, mx4_host.cpp:\n%s\n%s" % (" ".join(cmd), failure))
     os.replace(tmp, HOST)
     return HOST
 

@@ -10,21 +10,14 @@
 // A call on few rows is over sooner on the GPU (2 to 7 us) than the interpreter has checked its arguments, made
 // its outputs and passed it on (one row, calls one behind the other): quant8 7.5 us there and 4.6 here, dequant8 6.6
 // and 3.7, rmsnorm8 with a residual 10 and 5.4, gemm8 8.4 and 4.2.
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
-
-#include <ATen/ATen.h>
-#include <c10/core/GradMode.h>
-#include <c10/hip/HIPFunctions.h>
-#include <c10/hip/HIPStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
+#include "host_calls.hpp"
 #include "qamw_w8.h"
+
+extern PyMethodDef mx4_methods[];
 
 namespace {
 
-using at::Tensor;
+using namespace host;
 
 struct Entry {
     decltype(&qamw_quant8) quant8;
@@ -33,45 +26,6 @@ struct Entry {
     decltype(&qamw_gemm8_workspace) gemm8_workspace;
     decltype(&qamw_gemm8) gemm8;
 } lib;
-
-struct Skip {};     // not an ordinary call
-struct Raised {};   // a Python error is set
-
-PyObject* failed = nullptr;   // failed(return code, function) raises
-
-// The answer of the library: done, or a refusal, before anything was queued (w8.py gives its reason), or an
-// error of the runtime.
-void check(int rc, const char* name) {
-    if (rc == QAMW_OK) return;
-    if (rc == QAMW_ERR_ARG || rc == QAMW_ERR_UNSUPPORTED || rc == QAMW_ERR_WORKSPACE) throw Skip{};
-    Py_XDECREF(PyObject_CallFunction(failed, "is", rc, name));
-    throw Raised{};
-}
-
-const Tensor& tensor(PyObject* o) {
-    if (!THPVariable_CheckExact(o)) throw Skip{};
-    return THPVariable_Unpack(o);
-}
-
-void on(const Tensor& t, int device) {
-    if (!t.is_cuda() || t.get_device() != device || t.layout() != at::kStrided) throw Skip{};
-}
-
-struct Rows {
-    const void* p;
-    int32_t n, d;
-    int64_t ld;
-};
-
-// A bf16 or fp32 matrix with contiguous rows, of the size and type of `like`.
-Rows rows(const Tensor& t, int device, const Tensor* like = nullptr) {
-    on(t, device);
-    if (t.dim() != 2 || (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)) throw Skip{};
-    const int64_t n = t.size(0), d = t.size(1), ld = t.stride(0);
-    if (n < 1 || d < 1 || n > INT32_MAX || d > INT32_MAX || t.stride(1) != 1 || ld < d) throw Skip{};
-    if (like && (like->size(0) != n || like->size(1) != d || like->scalar_type() != t.scalar_type())) throw Skip{};
-    return {t.const_data_ptr(), (int32_t)n, (int32_t)d, ld};
-}
 
 // Codes with whole 16-byte chunks inside their storage.
 Rows codes(const Tensor& t, int device) {
@@ -85,26 +39,6 @@ Rows codes(const Tensor& t, int device) {
     return {p, (int32_t)n, (int32_t)d, ld};
 }
 
-const float* vec(const Tensor& t, int device, int64_t n) {
-    on(t, device);
-    if (t.scalar_type() != at::kFloat || t.numel() < n || !t.is_contiguous()) throw Skip{};
-    return t.const_data_ptr<float>();
-}
-
-// The tensor's device, which is the current one.
-int current_of(const Tensor& t) {
-    if (!t.is_cuda() || t.get_device() != c10::hip::current_device()) throw Skip{};
-    return t.get_device();
-}
-
-void* stream(int device) { return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream(); }
-
-qamw_dtype dtype(const Tensor& t) { return t.scalar_type() == at::kBFloat16 ? QAMW_BF16 : QAMW_F32; }
-
-Tensor make(const Tensor& like, at::IntArrayRef size, at::ScalarType type) {
-    return at::empty(size, like.options().dtype(type).requires_grad(false));
-}
-
 // Codes for n rows of d columns: rows of whole 16-byte chunks.
 Tensor make_codes(const Tensor& like, int64_t n, int64_t d) {
     const int64_t pitch = (d + 15) / 16 * 16;
@@ -114,44 +48,8 @@ Tensor make_codes(const Tensor& like, int64_t n, int64_t d) {
 
 int64_t pitch_of(int64_t d) { return (d + 15) / 16 * 16; }
 
-// A tuple of new references; null if one of them is.
-PyObject* tuple(std::initializer_list<PyObject*> items) {
-    PyObject* t = PyTuple_New((Py_ssize_t)items.size());
-    bool whole = t;
-    Py_ssize_t i = 0;
-    for (PyObject* o : items) {
-        whole = whole && o;
-        if (t) PyTuple_SET_ITEM(t, i++, o);
-        else Py_XDECREF(o);
-    }
-    if (!whole) Py_CLEAR(t);
-    return t;
-}
-
-// The interpreter's lock is free as long as one of these lives.
-struct Unlocked {
-    PyThreadState* state = PyEval_SaveThread();
-    Unlocked() = default;
-    Unlocked(const Unlocked&) = delete;
-    ~Unlocked() { PyEval_RestoreThread(state); }
-};
-
-template <typename F>
-PyObject* ordinary(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
-    HANDLE_TH_ERRORS
-    try {
-        if (given != wanted || !lib.gemm8) throw Skip{};
-        return f();
-    } catch (const Skip&) {
-        Py_RETURN_NONE;
-    } catch (const Raised&) {
-        return nullptr;
-    }
-    END_HANDLE_TH_ERRORS
-}
-
 PyObject* quant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return ordinary(n, 3, [&]() -> PyObject* {
+    return ordinary(n == 3 && lib.gemm8, [&]() -> PyObject* {
         const Tensor& x = tensor(a[0]);
         const int dev = current_of(x);
         const Rows r = rows(x, dev);
@@ -173,7 +71,7 @@ PyObject* quant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 PyObject* dequant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return ordinary(n, 4, [&]() -> PyObject* {
+    return ordinary(n == 4 && lib.gemm8, [&]() -> PyObject* {
         const Tensor& c = tensor(a[0]);
         const int dev = current_of(c);
         const Rows r = codes(c, dev);
@@ -192,7 +90,7 @@ PyObject* dequant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 PyObject* rmsnorm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return ordinary(n, 4, [&]() -> PyObject* {
+    return ordinary(n == 4 && lib.gemm8, [&]() -> PyObject* {
         const Tensor& x = tensor(a[0]);
         const int dev = current_of(x);
         const Rows r = rows(x, dev);
@@ -225,7 +123,7 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 PyObject* gemm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return ordinary(n, 5, [&]() -> PyObject* {
+    return ordinary(n == 5 && lib.gemm8, [&]() -> PyObject* {
         const Tensor& xq = tensor(a[0]);
         const Tensor& wq = tensor(a[2]);
         const int dev = current_of(xq);
@@ -277,4 +175,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_w8_host", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__w8_host(void) { return PyModule_Create(&module); }
+// The module: these functions, and those of the 4-bit operators (mx4_host.cpp).
+PyMODINIT_FUNC PyInit__w8_host(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddFunctions(m, mx4_methods) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -2,8 +2,9 @@
 every 32 columns, the norm in front of a linear layer with its output in that form, the product of two matrices in
 that form, and the same product for rows in groups with weights of their own (the experts of a mixture).
 
-The binding marshals arguments as the rest of the package does.  Work is queued on the current stream of the
-tensors' device.
+The binding marshals arguments as the rest of the package does; ordinary calls (matrices on the current device,
+outputs made here) take a short way through the compiled module _w8_host, with the same checks, and every other call,
+all errors among them, the way through this file.  Work is queued on the current stream of the tensors' device.
 
 A matrix of rows x d values is a pair of uint8 tensors: codes, rows x mx4_stride(d) (two columns a byte, whole groups
 of 256 columns), and scales, mx4_groups(d) x rows x 8.  Rows first to last of it are codes[first:last] and
@@ -19,7 +20,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .w8 import _INT_MAX, _VALUES, _current, _elsewhere, _failed, _fns, _out, _ptr, _raw_stream, _rows, _vec
+from .w8 import _INT_MAX, _VALUES, _current, _elsewhere, _failed, _fns, _host, _out, _ptr, _raw_stream, _rows, _vec
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 SIGNATURES = {
@@ -35,6 +36,14 @@ SIGNATURES = {
     "qamw_gemm4_grouped": ([_vp, _i64, _vp, _i64, _i32, _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i32, _i32, _i32,
                             _vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
 }
+
+
+def bind(lib):
+    """Gives the compiled module the functions of the loaded library."""
+    if _host is not None:
+        names = ("qamw_quant4", "qamw_dequant4", "qamw_rmsnorm4", "qamw_gemm4_workspace", "qamw_gemm4", "qamw_gemm4_grouped")
+        _host.bind4(*[ctypes.cast(getattr(lib, n), _vp).value for n in names])
+
 
 # limits of include/qamw_mx4.h
 MX4_MAX_NORM_COLS = 32768
@@ -139,6 +148,10 @@ def quant4(x: torch.Tensor, scale: Optional[torch.Tensor] = None, gate: Optional
            status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Rows of x (rows x d, bf16 or fp32) as (codes, scales): of x, of x silu(gate) with a gate, times the channel
     scale (d fp32) with one.  See qamw_quant4."""
+    if out is None and scales is None and status is None and _host is not None:
+        made = _host.quant4(x, scale, gate)
+        if made is not None:
+            return made
     ld_x = _rows(x, "x")
     rows, d = x.shape
     ld_g = _rows(gate, "gate", like=x) if gate is not None else 0
@@ -159,6 +172,10 @@ def dequant4(codes: torch.Tensor, scales: torch.Tensor, d: int, scale: Optional[
              out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values that codes stand for (rows x d, bf16 or fp32), with the channel scale that quant4 multiplied in
     divided out.  See qamw_dequant4."""
+    if out is None and out_dtype in _VALUES and _host is not None:
+        out = _host.dequant4(codes, scales, d, scale, out_dtype is torch.bfloat16)
+        if out is not None:
+            return out
     groups = mx4_groups(d)
     if d < 1:
         raise ValueError("d must be at least 1, got %d" % d)
@@ -184,6 +201,10 @@ def rmsnorm4(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     h = x + residual).  Without a residual h is x itself, and sum_out (if given) a copy of it; sum_out may be x or
     residual (h in place).  h carries no gradient: but where it is x itself, x or residual that requires one is
     refused while gradients are recorded.  See qamw_rmsnorm4."""
+    if sum_out is None and out is None and scales is None and status is None and _host is not None:
+        made = _host.rmsnorm4(x, weight, eps, residual)
+        if made is not None:
+            return made
     ld_x = _rows(x, "x")
     rows, d = x.shape
     ld_r = _rows(residual, "residual", like=x) if residual is not None else 0
@@ -218,6 +239,10 @@ def gemm4(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scales: 
           out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y = x w^T of activations (M rows) and weights (d_out rows) in 4 bits: M x d_out, bf16 or fp32.  Calls that may
     overlap need a workspace each, or none given.  See qamw_gemm4."""
+    if out is None and workspace is None and out_dtype in _VALUES and _host is not None:
+        out = _host.gemm4(xq, x_scales, wq, w_scales, out_dtype is torch.bfloat16)
+        if out is not None:
+            return out
     ld_x, ld_w = _codes4(xq, "xq"), _codes4(wq, "wq")
     M, b = xq.shape
     N, groups = wq.shape[0], b // 128
@@ -273,6 +298,10 @@ def gemm4_grouped(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_
     expert e's weights.  offsets (experts + 1) and index (one for each row of y) are int32 on the device; rows of y that
     no group has are left as they were, so without `out` offsets should run from 0 to the rows of y.  See
     qamw_gemm4_grouped."""
+    if out is None and out_dtype in _VALUES and _host is not None:
+        out = _host.gemm4_grouped(xq, x_scales, wq, w_scales, offsets, index, out_dtype is torch.bfloat16)
+        if out is not None:
+            return out
     ld_x = _codes4(xq, "xq")
     x_rows, b = xq.shape
     groups = b // 128
