@@ -51,7 +51,8 @@ __device__ __forceinline__ uint32_t codes_of(const float (&v)[kChunk], uint32_t&
 
 // Writes chunk c of a row and, of 16 lanes (chunks c & -16 .. c | 15), one the four scale bytes.
 __device__ __forceinline__ void store_codes(const Rows4Args& a, int64_t row, int c, uint32_t q, uint32_t scale) {
-    *reinterpret_cast<uint32_t*>(a.q + row * a.ld_q + c * 4) = q;
+    asm volatile("" : "+v"(c));   // addresses are formed here, not kept for every chunk of a thread
+    *reinterpret_cast<uint32_t*>(a.q + row * a.ld_q + (uint32_t)c * 4) = q;
     uint32_t s = scale << (8 * (c / 4 % 4));
     s |= dpp<kRor4>(s);
     s |= dpp<kRor8>(s);
@@ -178,15 +179,23 @@ hipError_t launch_quant(const Rows4Args& a, hipStream_t st) {
 constexpr int max_waves(int v) { return v <= 2 ? 16 : v <= 4 ? 12 : 8; }
 
 // row_waves wavefronts a row: one row a workgroup, or, with one wavefront a row, blockDim / 64.  Chunk t + k threads
-// of a row is thread t's; a thread without one at some k loads the last whole one again, so that every load is
-// unconditional.
+// of the row's whole groups is thread t's; a thread without one at some k loads the last one again, so that every load
+// is unconditional.  A part of a group at the end is the first 32 threads', a chunk each.
 template <bool BF, bool FACTOR, int V>
-__global__ __launch_bounds__(max_waves(V) * kWave) void k_rmsnorm4(Rows4Args a, int row_waves) {
+__global__ __launch_bounds__(max_waves(V) * kWave) void k_rmsnorm4(Rows4Args a, int row_waves, int keep) {
+    // FACTOR: a thread's factors, kept over its rows (with `keep`: as long as they fit)
+    extern __shared__ __align__(16) float4 s_factor[];
+    bool kept = false;
     __shared__ double s_sum[2][kMaxWaves];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    // (in scalar registers: a row's addresses are then a scalar base and an offset of 32 bits)
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int rows_wg = blockDim.x / kWave / row_waves, part = wave % row_waves;
     const int t = part * kWave + lane, nt = row_waves * kWave;
-    const int full = a.d / kChunk, rest = a.d % kChunk, chunks = (a.d + kGroupCols - 1) / kGroupCols * kGroupChunks;
+    const int chunks = a.d / kGroupCols * kGroupChunks, end_c = chunks + t, have = a.d - end_c * kChunk;
+    const bool end = a.d % kGroupCols && t < kGroupChunks;
+    int chunk[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) chunk[k] = t + k * nt < chunks ? t + k * nt : chunks - 1;
     bool flag = false;
     int buf = 0;
     for (int64_t row = (int64_t)blockIdx.x * rows_wg + wave / row_waves; row < a.rows;
@@ -194,20 +203,15 @@ __global__ __launch_bounds__(max_waves(V) * kWave) void k_rmsnorm4(Rows4Args a, 
         const void* x = at<BF>(a.x, row * a.ld_x);
         const void* other = at<BF>(a.other, row * a.ld_other);
         void* sum_out = const_cast<void*>(at<BF>(a.sum, row * a.ld_sum));
-        float v[V][kChunk];
-        if (full > 0) {
+        float v[V][kChunk], last[kChunk];
+        double sum = 0.0;
+        if (chunks > 0) {
             Raw<BF> rx[V], ro[V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int c = t + k * nt < full ? t + k * nt : full - 1;
-                rx[k] = *reinterpret_cast<const Raw<BF>*>(at<BF>(x, c * kChunk));
-            }
+            for (int k = 0; k < V; ++k) rx[k] = *reinterpret_cast<const Raw<BF>*>(at<BF>(x, chunk[k] * kChunk));
             if (a.other) {
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int c = t + k * nt < full ? t + k * nt : full - 1;
-                    ro[k] = *reinterpret_cast<const Raw<BF>*>(at<BF>(other, c * kChunk));
-                }
+                for (int k = 0; k < V; ++k) ro[k] = *reinterpret_cast<const Raw<BF>*>(at<BF>(other, chunk[k] * kChunk));
             }
 #pragma unroll
             for (int k = 0; k < V; ++k) unpack<BF>(rx[k], v[k]);
@@ -220,52 +224,59 @@ __global__ __launch_bounds__(max_waves(V) * kWave) void k_rmsnorm4(Rows4Args a, 
                     for (int i = 0; i < kChunk; ++i) v[k][i] += o[i];
                 }
             }
-        }
-        // the chunk that the row ends in, and the ones behind it
+            if (a.sum) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = t + k * nt;
-            if (c < full) continue;
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) v[k][i] = 0.0f;
-            if (c == full && rest) {
-                load_part<BF>(at<BF>(x, c * kChunk), rest, v[k]);
-                if (a.other) {
-                    float o[kChunk];
-                    load_part<BF>(at<BF>(other, c * kChunk), rest, o);
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) v[k][i] += o[i];
-                }
+                for (int k = 0; k < V; ++k)
+                    if (t + k * nt < chunks) store_chunk<BF>(const_cast<void*>(at<BF>(sum_out, chunk[k] * kChunk)), v[k]);
             }
-        }
-        if (a.sum) {
+            // (a chunk loaded again does not count: with h in place of x, its thread may have written it already)
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const int c = t + k * nt;
-                void* y = const_cast<void*>(at<BF>(sum_out, c * kChunk));
-                if (c < full)
-                    store_chunk<BF>(y, v[k]);
-                else if (c == full && rest)
-                    store_part<BF>(y, rest, v[k]);
+                double q = 0.0;
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) q = __builtin_fma((double)v[k][i], (double)v[k][i], q);
+                sum += t + k * nt < chunks ? q : 0.0;
             }
         }
-        double sum = 0.0;
+        if (end) {
+            load_part<BF>(at<BF>(x, end_c * kChunk), have, last);
+            if (a.other) {
+                float o[kChunk];
+                load_part<BF>(at<BF>(other, end_c * kChunk), have, o);
 #pragma unroll
-        for (int k = 0; k < V; ++k)
+                for (int i = 0; i < kChunk; ++i) last[i] += o[i];
+            }
+            if (a.sum) store_part<BF>(const_cast<void*>(at<BF>(sum_out, end_c * kChunk)), have, last);
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) sum = __builtin_fma((double)v[k][i], (double)v[k][i], sum);
+            for (int i = 0; i < kChunk; ++i) sum = __builtin_fma((double)last[i], (double)last[i], sum);
+        }
         if constexpr (FACTOR) {
+            if (chunks > 0) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int c = t + k * nt;
-                float f[kChunk];
-                if (c < full) {
-                    unpack<false>(*reinterpret_cast<const Float8*>(a.factor + c * kChunk), f);
-                } else {
-                    load_part<false>(a.factor + c * kChunk, c == full ? rest : 0, f);
+                for (int k = 0; k < V; ++k) {
+                    Float8 f;
+                    float4* mine = s_factor + 2 * k * nt + t;   // wavefronts of other rows write the same there
+                    asm volatile("" ::: "memory");   // a chunk's factors at a time: together they need scratch memory
+                    if (kept) {
+                        const float4 lo = mine[0], hi = mine[nt];
+                        f = {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+                    } else {
+                        f = *reinterpret_cast<const Float8*>(a.factor + chunk[k] * kChunk);
+                        if (keep) {
+                            mine[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+                            mine[nt] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) v[k][i] *= f.v[i];
                 }
+                kept = keep;
+            }
+            if (end) {
+                float f[kChunk];
+                load_part<false>(a.factor + end_c * kChunk, have, f);
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) v[k][i] *= f[i];
+                for (int i = 0; i < kChunk; ++i) last[i] *= f[i];
             }
         }
 #pragma unroll
@@ -278,38 +289,73 @@ __global__ __launch_bounds__(max_waves(V) * kWave) void k_rmsnorm4(Rows4Args a, 
             for (int w = 1; w < row_waves; ++w) sum += s_sum[buf][w];
         }
         const float f = (float)(1.0 / sqrt(sum / (double)a.d + a.eps));
+        if (chunks > 0) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = t + k * nt;
-            if (c >= chunks) break;   // (of 32 lanes all or none)
+            for (int k = 0; k < V; ++k) {
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) v[k][i] *= f;
+                uint32_t s;
+                bool bad;
+                const uint32_t q = codes_of(v[k], s, bad);
+                if (t + k * nt < chunks) {   // (of 32 lanes all or none)
+                    flag |= bad;
+                    store_codes(a, row, chunk[k], q, s);
+                }
+            }
+        }
+        if (end) {
             // behind the row: zeros, whatever the factor is
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) v[k][i] = c < full || (c == full && i < rest) ? v[k][i] * f : 0.0f;
+            for (int i = 0; i < kChunk; ++i) last[i] = i < have ? last[i] * f : 0.0f;
             uint32_t s;
             bool bad;
-            const uint32_t q = codes_of(v[k], s, bad);
+            const uint32_t q = codes_of(last, s, bad);
             flag |= bad;
-            store_codes(a, row, c, q, s);
+            store_codes(a, row, end_c, q, s);
         }
     }
     if (flag && a.status) atomicOr(a.status, QAMW_FLAG_NONFINITE);
 }
 
+// How a row is spread: v chunks a thread, w wavefronts.  Many rows fill the chip by themselves, and a thread has 4 chunks,
+// so that a compute unit has many bytes under way and few wavefronts wait for each other (4096 x 5120 bf16 with a
+// residual: 1 chunk 43.6 us, 2: 33.2, 4: 31.3, 5: 31.6, 8: 37.9); fewer values than 4.5 million are spread over more
+// wavefronts (512 x 4096: 2 chunks 5.3 us, 4: 6.3; 1024 x 5120: 10.4 and 9.8; one row of 4096: 3.5 and 4.3).
+struct NormShape {
+    int v, w;
+};
+NormShape norm_shape(int rows, int d) {
+    const int chunks = d / kGroupCols * kGroupChunks, waves = chunks < kWave ? 1 : (chunks + kWave - 1) / kWave;
+    if (waves == 1) return {1, 1};
+    for (const int v : {2, 4})
+        if ((v == 4 || (int64_t)rows * d < 4500000) && (waves + v - 1) / v <= max_waves(v)) return {v, (waves + v - 1) / v};
+    return {8, (waves + 7) / 8};   // up to 32768 columns
+}
+
 template <bool BF, bool FACTOR, int V>
 hipError_t launch_norm(const Rows4Args& a, int w, hipStream_t st) {
     const int rows_wg = w == 1 ? 4 : 1;
+    // the factors of a row: in LDS from the first row of a workgroup on, and then a workgroup has many rows
+    // (about as many workgroups as fit at once)
+    const size_t bytes = FACTOR ? (size_t)V * 32 * w * kWave : 0;
+    const bool keep = bytes > 0 && bytes <= 65536;
     int64_t wgs = ((int64_t)a.rows + rows_wg - 1) / rows_wg;
-    wgs = wgs < (1 << 20) ? wgs : 1 << 20;
-    return launch_kernel(k_rmsnorm4<BF, FACTOR, V>, dim3((unsigned)wgs), rows_wg * w * kWave, 0, st, a, w);
+    const int64_t most = keep ? 256 * (12 / (rows_wg * w) > 0 ? 12 / (rows_wg * w) : 1) : 1 << 20;
+    wgs = wgs < most ? wgs : most;
+    return launch_kernel(k_rmsnorm4<BF, FACTOR, V>, dim3((unsigned)wgs), rows_wg * w * kWave, keep ? bytes : 0, st, a, w,
+                         keep ? 1 : 0);
 }
 
 template <bool BF, bool FACTOR>
 hipError_t launch_norm(const Rows4Args& a, hipStream_t st) {
-    const int chunks = (a.d + kGroupCols - 1) / kGroupCols * kGroupChunks, waves = (chunks + kWave - 1) / kWave;
-    if (waves <= 8) return launch_norm<BF, FACTOR, 1>(a, waves, st);
-    if (waves <= 32) return launch_norm<BF, FACTOR, 2>(a, (waves + 1) / 2, st);
-    if (waves <= 48) return launch_norm<BF, FACTOR, 4>(a, (waves + 3) / 4, st);
-    return launch_norm<BF, FACTOR, 8>(a, (waves + 7) / 8, st);   // up to 32768 columns
+    const NormShape s = norm_shape(a.rows, a.d);
+    switch (s.v) {
+    case 1: return launch_norm<BF, FACTOR, 1>(a, s.w, st);
+    case 2: return launch_norm<BF, FACTOR, 2>(a, s.w, st);
+    case 4: return launch_norm<BF, FACTOR, 4>(a, s.w, st);
+    default: return launch_norm<BF, FACTOR, 8>(a, s.w, st);
+    }
 }
 
 // 8 codes a thread; a workgroup covers tx chunks of rows_wg rows, 256 / tx at a time, and keeps the reciprocals of its
