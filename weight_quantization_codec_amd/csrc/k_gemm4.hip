@@ -49,35 +49,55 @@ __device__ __forceinline__ Groups groups_from(const Gemm4Args& a, int bm, int e)
     }
     return g;
 }
-// The rows m0 .. m_end - 1 of workgroup b's tile, its expert and its tile of columns; false without one.
-__device__ __forceinline__ bool group_tile(const Gemm4Args& a, int bm, int b, int tiles_m, int tiles_n, int& expert,
-                                           int& m0, int& m_end, int& tile_n) {
-    const int lane = threadIdx.x % kWave;
-    Groups g{};
-    int total = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += kWave) {
-        g = groups_from(a, bm, e0 + lane);
-        total += __shfl(g.sum, kWave - 1);
-    }
-    total = total < tiles_m ? total : tiles_m;   // (more only where groups overlap)
-    if (b >= total * tiles_n) return false;
-    int tile;
-    tile_of(b, 1, total, tiles_n, tile, tile_n);
-    for (int e0 = 0;; e0 += kWave) {
-        if (a.experts > kWave) g = groups_from(a, bm, e0 + lane);
-        const uint64_t reached = __ballot(g.sum > tile);
-        if (reached) {
-            const int at = __builtin_ctzll(reached);
-            const int before = at > 0 ? __shfl(g.sum, at - 1) : 0;
-            expert = __builtin_amdgcn_readfirstlane(e0 + at);
-            m_end = __builtin_amdgcn_readfirstlane(__shfl(g.hi, at));
-            m0 = __builtin_amdgcn_readfirstlane(__shfl(g.lo, at) + (tile - before) * bm);
-            m_end = m_end < m0 + bm ? m_end : m0 + bm;
-            return true;
+// Which tile a workgroup has: rows m0 .. m0 + rows_m - 1, columns n0 .. n0 + rows_n - 1, part `split` of k, an expert.
+struct Tile {
+    int m0, rows_m, n0, rows_n, split, expert;
+};
+// The tiles of a launch in their order.
+template <int BM, int BN, bool GROUPED>
+struct Tiles {
+    Groups g;             // the last 64 groups counted (of up to 64, all)
+    int tiles_m, tiles_n, splits, count;
+    __device__ __forceinline__ Tiles(const Gemm4Args& a, int tm, int tn, int sp) : g{}, tiles_m(tm), tiles_n(tn), splits(sp) {
+        if constexpr (GROUPED) {
+            int total = 0;
+            for (int e0 = 0; e0 < a.experts; e0 += kWave) {
+                g = groups_from(a, BM, e0 + (int)threadIdx.x % kWave);
+                total += __shfl(g.sum, kWave - 1);
+            }
+            total = __builtin_amdgcn_readfirstlane(total);
+            tiles_m = total < tiles_m ? total : tiles_m;   // (more only where groups overlap)
         }
-        tile -= __shfl(g.sum, kWave - 1);
+        count = tiles_m * tiles_n * splits;
     }
-}
+    __device__ __forceinline__ Tile at(const Gemm4Args& a, int number) {
+        Tile t{};
+        int tile_m, tile_n;
+        t.split = tile_of(number, splits, tiles_m, tiles_n, tile_m, tile_n);
+        int m_end = a.M;
+        if constexpr (GROUPED) {
+            for (int e0 = 0;; e0 += kWave) {
+                if (a.experts > kWave) g = groups_from(a, BM, e0 + (int)threadIdx.x % kWave);
+                const uint64_t reached = __ballot(g.sum > tile_m);
+                if (reached) {
+                    const int lane = __builtin_ctzll(reached);
+                    const int before = lane > 0 ? __shfl(g.sum, lane - 1) : 0;
+                    t.expert = __builtin_amdgcn_readfirstlane(e0 + lane);
+                    m_end = __builtin_amdgcn_readfirstlane(__shfl(g.hi, lane));
+                    t.m0 = __builtin_amdgcn_readfirstlane(__shfl(g.lo, lane) + (tile_m - before) * BM);
+                    break;
+                }
+                tile_m -= __shfl(g.sum, kWave - 1);
+            }
+        } else {
+            t.m0 = tile_m * BM;
+        }
+        t.n0 = tile_n * BN;
+        t.rows_m = m_end - t.m0 < BM ? m_end - t.m0 : BM;
+        t.rows_n = a.N - t.n0 < BN ? a.N - t.n0 : BN;
+        return t;
+    }
+};
 
 // 4 bytes a lane from a buffer into LDS at lds + 4 lane, like load_lds16.
 __device__ __forceinline__ void load_lds4(u32x4 rsrc, uint32_t voff, uint32_t lds) {
@@ -114,7 +134,30 @@ struct TileCfg {
 
 constexpr uint32_t kFar = 0xF0000000u;   // an offset past every buffer: what is loaded from there is 0
 
-template <int BM, int BN, int WM, int S, int SP, int FA, int OUT, bool GROUPED>
+// Waits until at most N of the wavefront's loads and stores are under way; where the output of the tile before was
+// stored with STORES stores behind the loads that are waited for, those may be under way too.
+template <int N, int STORES>
+__device__ __forceinline__ void wait_stage_behind(bool stored) {
+    if constexpr (STORES > 0 && N + STORES < 64) {
+        if (stored) {
+            wait_stage<N + STORES>();
+            return;
+        }
+    }
+    wait_stage<N>();
+}
+
+// A kernel's first argument, read from memory again: what a loop needs only now and then is not kept in scalar
+// registers, which would not suffice (and a spilled one costs a vector instruction each time).
+__device__ __forceinline__ Gemm4Args args_again() {
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const Gemm4Args*)p;
+}
+
+// WALK: a workgroup has every gridDim-th tile, one behind the other, and the loads of the next tile's first stages are
+// under way while the last ones are multiplied and the output is formed.  Otherwise it has one.
+template <int BM, int BN, int WM, int S, int SP, int FA, int OUT, bool GROUPED, bool WALK>
 __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int tiles_n, int splits) {
     using C = TileCfg<BM, BN, WM, S, SP, FA>;
     constexpr int TM = C::kTM, TN = C::kTN, NS = C::kNS;
@@ -122,19 +165,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     static_assert(SP <= NS * C::kMfma && S * C::kLoads < 64 && S >= 2);
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    int tile_m = 0, tile_n = 0, split = 0, expert = 0, m0 = 0, m_end = a.M;
-    if constexpr (GROUPED) {
-        if (!group_tile(a, BM, blockIdx.x, tiles_m, tiles_n, expert, m0, m_end, tile_n)) return;
-    } else {
-        split = tile_of(blockIdx.x, splits, tiles_m, tiles_n, tile_m, tile_n);
-        m0 = tile_m * BM;
-    }
-    const int n0 = tile_n * BN;
-    const int rows_m = m_end - m0 < BM ? m_end - m0 : BM, rows_n = a.N - n0 < BN ? a.N - n0 : BN;
-    // this workgroup's part of k: groups of columns first .. first + steps - 1
-    // (at most 2^15 groups in 16 parts: 32 bits do, and a division of 64 bits takes a thousand cycles)
-    const int first = (int)((uint32_t)(a.groups * split) / (uint32_t)splits);
-    const int steps = (int)((uint32_t)(a.groups * (split + 1)) / (uint32_t)splits) - first;
+    Tiles<BM, BN, GROUPED> tiles(a, tiles_m, tiles_n, splits);
+    int number = blockIdx.x;
+    if (number >= tiles.count) return;
+    Tile tile = tiles.at(a, number);
 
     // Loads.  One moves 8 rows of 128 bytes; LDS row r holds its 16-byte chunk c at place c ^ (r / 2 % 8).
     // A 16-byte read goes through LDS in phases of 16 lanes over 64 banks, here 16 rows at one c: 8 even
@@ -142,59 +176,102 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
     constexpr int kLoadsX = BM / 32;
     const bool indexed = GROUPED && a.index;
-    // the row of x that row r of the tile is, and whether there is none
-    auto x_row = [&](int r, bool& none) {
-        const int row = a.index[m0 + (r < rows_m ? r : rows_m - 1)];
-        none = r >= rows_m || row < 0 || row >= a.x_rows;
-        return row;
-    };
     uint32_t voff[C::kLoads];   // scales first
+    // The offsets in x go by the tile where rows have an index, and by the place in the tile alone otherwise.  A
+    // wavefront loads codes of (up to) 64 rows and scales of 64: a lane fetches the index of one of either, and the
+    // others ask it.
+    auto offsets = [&](const Gemm4Args& a, const Tile& at, bool of_x_only) {
+        int lane = threadIdx.x % kWave, of_codes = 0, of_scales = 0;
+        asm volatile("" : "+v"(lane));   // what follows from it is formed here, and takes no registers in the loop
+        auto fetch = [&](int r) { return a.index[at.m0 + (r < at.rows_m ? r : at.rows_m - 1)]; };
+        if (indexed) {
+            of_codes = fetch((lane / 8 * 4 + wave) * 8 + lane % 8);
+            of_scales = fetch((lane / 32 * 4 + wave) * 32 + lane % 32);
+        }
+        auto far = [&](int r, int row) { return r >= at.rows_m || row < 0 || row >= a.x_rows; };
 #pragma unroll
-    for (int i = 0; i < C::kScaleLoads; ++i) {
-        const int at = i * 4 + wave, part = at < C::kScaleRows ? at : C::kScaleRows - 1;
-        const bool is_x = part < kLoadsX;
-        int row = (is_x ? part : part - kLoadsX) * 32 + lane / 2;
-        bool none = false;
-        if (indexed && is_x) row = x_row(row, none);
-        voff[i] = none ? kFar : (uint32_t)row * 8 + lane % 2 * 4;
-    }
+        for (int i = 0; i < C::kScaleLoads; ++i) {
+            const int n = i * 4 + wave, part = n < C::kScaleRows ? n : C::kScaleRows - 1;
+            const bool is_x = kLoadsX % 4 ? part < kLoadsX : i < kLoadsX / 4;
+            if (of_x_only && !is_x) continue;
+            const int r = (is_x ? part : part - kLoadsX) * 32 + lane / 2;
+            voff[i] = (uint32_t)r * 8 + lane % 2 * 4;
+            if (indexed && is_x) {
+                const int row = __shfl(of_scales, i * 32 % kWave + lane / 2);
+                voff[i] = far(r, row) ? kFar : (uint32_t)row * 8 + lane % 2 * 4;
+            }
+        }
 #pragma unroll
-    for (int i = 0; i < C::kCodeLoads; ++i) {
-        const bool is_x = i < kLoadsX;
-        const int r = ((is_x ? i : i - kLoadsX) * 4 + wave) * 8 + lane / 8;
-        int row = r;
-        bool none = false;
-        if (indexed && is_x) row = x_row(row, none);
-        voff[C::kScaleLoads + i] =
-            none ? kFar : (uint32_t)row * (uint32_t)(is_x ? a.ld_x : a.ld_w) + (uint32_t)((lane % 8) ^ (r / 2 % 8)) * 16;
-    }
-    const int64_t at_m = indexed ? 0 : m0;
-    const int64_t of_w = GROUPED ? expert * a.ld_wexpert : 0, of_we = GROUPED ? expert * a.ld_weexpert : 0;
-    const uint64_t base_x = (uint64_t)(a.xq + at_m * a.ld_x + (int64_t)first * kGroupBytes);
-    const uint64_t base_w = (uint64_t)(a.wq + of_w + n0 * a.ld_w + (int64_t)first * kGroupBytes);
-    const uint64_t base_xe = (uint64_t)(a.xe + at_m * 8 + first * a.ld_xe);
-    const uint64_t base_we = (uint64_t)(a.we + of_we + n0 * 8ll + first * a.ld_we);
-    // Buffers end with the last row that there is; a row's bytes behind this part of k are in them, and never read.
-    const int64_t have_x = indexed ? a.x_rows : rows_m;
-    const uint32_t left = (uint32_t)(a.groups - first) * kGroupBytes;
-    const uint32_t size_x = have_x ? (uint32_t)((have_x - 1) * a.ld_x) + left : 0;
-    const uint32_t size_w = (uint32_t)((rows_n - 1) * a.ld_w) + left;
-    // The buffers of step t, empty past the last step.  Loads past them touch no memory; the count of loads under
-    // way is the same in every step.
+        for (int i = 0; i < C::kCodeLoads; ++i) {
+            const bool is_x = i < kLoadsX;
+            if (of_x_only && !is_x) continue;
+            const int r = ((is_x ? i : i - kLoadsX) * 4 + wave) * 8 + lane / 8;
+            const uint32_t chunk = (uint32_t)((lane % 8) ^ (r / 2 % 8)) * 16;
+            uint32_t& v = voff[C::kScaleLoads + i];
+            v = (uint32_t)r * (uint32_t)(is_x ? a.ld_x : a.ld_w) + chunk;
+            if (indexed && is_x) {
+                const int row = __shfl(of_codes, i * 8 % kWave + lane / 8);
+                v = far(r, row) ? kFar : (uint32_t)row * (uint32_t)a.ld_x + chunk;
+            }
+        }
+    };
+    // Where the next loads come from: step `load_t` of `load_steps` of a tile.  Buffers end with the last row that
+    // there is; a row's bytes behind this part of k are in them, and never read.  Behind the last tile they are
+    // empty: loads from there touch no memory, and the count of loads under way is the same in every step.
+    uint64_t base_x, base_w, base_xe, base_we;
+    uint32_t size_x, size_w, size_xe, size_we;
+    int load_t, load_steps, load_number = number;
+    auto load_from = [&](const Gemm4Args& a, const Tile& at) {
+        // (at most 2^15 groups in 16 parts: 32 bits do, and a division of 64 bits takes a thousand cycles)
+        const int first = (int)((uint32_t)(a.groups * at.split) / (uint32_t)splits);
+        load_steps = (int)((uint32_t)(a.groups * (at.split + 1)) / (uint32_t)splits) - first;
+        load_t = 0;
+        const int64_t at_m = indexed ? 0 : at.m0, have_x = indexed ? a.x_rows : at.rows_m;
+        const uint32_t left = (uint32_t)(a.groups - first) * kGroupBytes;
+        base_x = (uint64_t)(a.xq + at_m * a.ld_x + (int64_t)first * kGroupBytes);
+        base_w = (uint64_t)(a.wq + (GROUPED ? at.expert * a.ld_wexpert : 0) + at.n0 * a.ld_w + (int64_t)first * kGroupBytes);
+        base_xe = (uint64_t)(a.xe + at_m * 8 + first * a.ld_xe);
+        base_we = (uint64_t)(a.we + (GROUPED ? at.expert * a.ld_weexpert : 0) + at.n0 * 8ll + first * a.ld_we);
+        size_x = have_x ? (uint32_t)((have_x - 1) * a.ld_x) + left : 0;
+        size_w = (uint32_t)((at.rows_n - 1) * a.ld_w) + left;
+        size_xe = (uint32_t)have_x * 8;
+        size_we = (uint32_t)at.rows_n * 8;
+    };
     u32x4 rx, rw, rxe, rwe;
-    auto buffers = [&](int t) {
-        const bool in = t < steps;
-        rx = rsrc_of(base_x + (uint64_t)t * kGroupBytes, in && size_x ? size_x - (uint32_t)t * kGroupBytes : 0u);
-        rw = rsrc_of(base_w + (uint64_t)t * kGroupBytes, in ? size_w - (uint32_t)t * kGroupBytes : 0u);
-        rxe = rsrc_of(base_xe + t * a.ld_xe, in ? (uint32_t)have_x * 8 : 0u);
-        rwe = rsrc_of(base_we + t * a.ld_we, in ? (uint32_t)rows_n * 8 : 0u);
+    auto buffers = [&]() {   // of the next step
+        rx = rsrc_of(base_x, size_x);
+        rw = rsrc_of(base_w, size_w);
+        rxe = rsrc_of(base_xe, size_xe);
+        rwe = rsrc_of(base_we, size_we);
         // a scalar register written by a vector instruction needs five wait states before a load reads it; the
         // compiler does not look into the assembly of the loads
         asm volatile("s_nop 4" ::"s"(rx), "s"(rw), "s"(rxe), "s"(rwe));
+        base_x += kGroupBytes;
+        base_w += kGroupBytes;
+        base_xe += a.ld_xe;
+        base_we += a.ld_we;
+        size_x = size_x ? size_x - kGroupBytes : 0;
+        size_w = size_w ? size_w - kGroupBytes : 0;
+    };
+    // The buffers of the step behind: of this tile, of the next one, or none.  (Apart from `buffers`, because new
+    // offsets may replace the old ones only when the loads that use those have been issued.)
+    auto next_step = [&]() {
+        if (++load_t < load_steps) return;
+        load_number += gridDim.x;
+        if (WALK && load_number < tiles.count) {
+            const Gemm4Args b = args_again();
+            const Tile at = tiles.at(b, load_number);
+            load_from(b, at);
+            if (indexed) offsets(b, at, true);
+        } else {
+            size_x = size_w = size_xe = size_we = 0;
+            load_t = 0;   // for good: no further tile is looked for
+            load_steps = 0x7FFFFFFF;
+        }
     };
     auto load = [&](int i, uint32_t stage) {
         if (i < C::kScaleLoads) {
-            const int at = i * 4 + wave, part = at < C::kScaleRows ? at : C::kScaleRows - 1;
+            const int n = i * 4 + wave, part = n < C::kScaleRows ? n : C::kScaleRows - 1;
             // (of the larger tiles, all four wavefronts load of the same operand)
             const bool is_x = kLoadsX % 4 ? part < kLoadsX : i < kLoadsX / 4;
             load_lds4(is_x ? rxe : rwe, voff[i], stage + C::kCodes + (uint32_t)part * 256);
@@ -203,6 +280,9 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
             load_lds16(j < kLoadsX ? rx : rw, voff[i], stage + (uint32_t)(j * 4 + wave) * 1024);
         }
     };
+    offsets(a, tile, false);
+    load_from(a, tile);
+    int steps = load_steps;
 
     // Operands: block row lane % 32, 16-byte chunk ks + 4 (lane / 32) of sub-step ks.
     const int wm = wave / C::kWN, wn = wave % C::kWN;
@@ -213,7 +293,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     const uint32_t row_x = wm * C::kRowsM * kGroupBytes, row_w = (BM + wn * C::kRowsN) * kGroupBytes;
     const uint32_t scale_x = C::kCodes + (wm * C::kRowsM + lane % 32) * 8 + lane / 32 * 4;
     const uint32_t scale_w = C::kCodes + (BM + wn * C::kRowsN + lane % 32) * 8 + lane / 32 * 4;
-    i32x4 fx[NS][TM], fw[NS][TN];
+    // WALK: operands of a step in parts, below.  Otherwise the operands of a step are read as a whole while the step
+    // before is multiplied, so that a step has one barrier and waits for nothing that it has just asked for.
+    constexpr int SETS = WALK ? 1 : 2;
+    i32x4 fx[SETS * NS][TM], fw[SETS * NS][TN];
     int sx[TM], sw[TN], next_sx[TM], next_sw[TN];
     auto read = [&](int i, int set, const uint8_t* st, int ks) {
         if (i < TN)
@@ -229,124 +312,207 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     };
 
     // The first S - 1 stages, and of the next one what a step issues before it ends.
-    constexpr int kRefillStart = (NS - 1 - FA) * C::kMfma;   // slots of a refill within its own step
+    constexpr int kRefillStart = WALK ? (NS - 1 - FA) * C::kMfma : NS * C::kMfma;   // slots of a refill within its own step
+    static_assert(C::issued(kRefillStart) == C::kLoads);   // (the walk's stores are behind whole refills)
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        buffers(s);
+        if (s > 0) next_step();
+        buffers();
 #pragma unroll
-        for (int i = 0; i < (s < S - 1 ? C::kLoads : C::issued(kRefillStart)); ++i) load(i, lds0 + s * C::kStage);
+        for (int i = 0; i < C::kLoads; ++i) load(i, lds0 + s * C::kStage);
     }
-    f32x16 acc[TN][TM];   // zeroed while the first loads are under way
-#pragma unroll
-    for (int n = 0; n < TN; ++n)
-#pragma unroll
-        for (int m = 0; m < TM; ++m) {
-            acc[n][m] = (f32x16)(0.0f);
-            asm volatile("" : "+a"(acc[n][m]));
-        }
-    wait_stage<(S - 2) * C::kLoads + C::issued(kRefillStart)>();
     constexpr int kOps = TM + TN;
-#pragma unroll
-    for (int i = 0; i < kOps; ++i) read(i, 0, lds, 0), read_scale(i, lds);
-
-    int buf = 0, refill = S - 1;
-    for (int t = 0; t < steps; ++t) {
-        const int next = buf + 1 < S ? buf + 1 : 0;
-        const uint8_t* cur_p = lds + buf * C::kStage;
-        const uint8_t* next_p = lds + next * C::kStage;
-#pragma unroll
-        for (int i = 0; i < TN; ++i) sw[i] = next_sw[i];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) sx[i] = next_sx[i];
-        static_for<NS>([&](auto ks_) {
-            constexpr int ks = ks_;
-            if constexpr (ks == FA + 1) {
-                // every wavefront has read this stage: its refill may begin
-                if constexpr (ks < NS - 1) wait_reads();
-                else wait_stage<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma)>();
-                buffers(t + S);
-                refill = buf;
-            } else if constexpr (ks == NS - 1) {
-                wait_stage<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma)>();
-            }
-            constexpr int reads = ks < FA || ks == NS - 1 ? kOps : ks == FA ? (NS - 1 - FA) * kOps : 0;
-            static_for<C::kMfma>([&](auto j_) {
-                constexpr int j = j_;
-                static_for<reads>([&](auto i) {
-                    constexpr int at = reads > C::kMfma ? i * C::kMfma / reads : int(i), set = (ks + 1 + i / kOps) % NS;
-                    if constexpr (at == j) {
-                        read(i % kOps, set, ks == NS - 1 ? next_p : cur_p, set);
-                        if constexpr (ks == NS - 1) read_scale(i, next_p);
-                    }
-                });
-                constexpr int slot = ((ks + NS - 1 - FA) % NS) * C::kMfma + j;
-                static_for<C::kLoads>([&](auto i) {
-                    if constexpr (C::slot(i) == slot) load(i, lds0 + refill * C::kStage);
-                });
-                constexpr int n = j / TM, m = j % TM;
-                acc[n][m] = mfma4<ks>(fw[ks][n], fx[ks][m], acc[n][m], sw[n], sx[m]);
-                __builtin_amdgcn_sched_barrier(0);
-            });
-        });
-        buf = next;
-    }
-
-    // Rows of y through LDS, 32 at a time and wavefront, for stores of whole lines.  A lane has column
-    // m = lane % 32 of each block and rows n = 8 g + 4 (lane / 32) + 0..3.
-    wait_stage<0>();
-    constexpr int kEs = OUT == kBf16 ? 2 : 4, kRow = C::kRowsN * kEs, kChunks = kRow / 16;
-    constexpr int kParts = C::kLds / (4 * 32 * kRow) < TM ? C::kLds / (4 * 32 * kRow) : TM;
-    const int r = lane % 32, h = lane / 32;
-    const int64_t pitch = (OUT == kSums ? (int64_t)sums_pitch(a.N) : a.ld_y) * kEs;
-    const bool full = rows_m == BM && rows_n == BN;
-    uint8_t* out = reinterpret_cast<uint8_t*>(OUT == kSums ? a.work : a.y);
-    if (OUT == kSums) out += (int64_t)split * a.M * pitch;
-    uint8_t* y = out + ((int64_t)m0 + wm * C::kRowsM) * pitch + ((int64_t)n0 + wn * C::kRowsN) * kEs;
-    uint8_t* y_lane = y + (lane / kChunks) * pitch + (lane % kChunks) * 16;
-#pragma unroll
-    for (int m = 0; m < TM; ++m) {
-        uint8_t* mine = lds + (m % kParts * 4 + wave) * 32 * kRow;
+    f32x16 acc[TN][TM];
+    if constexpr (!WALK) {   // zeroed while the first loads are under way
 #pragma unroll
         for (int n = 0; n < TN; ++n)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int byte = (n * 32 + 8 * g + 4 * h) * kEs;
-                uint8_t* p = mine + r * kRow + (((byte / 16) ^ r) % kChunks) * 16 + byte % 16;
-                const float v[4] = {acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
-                if constexpr (OUT == kBf16)
-                    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
-                else
-                    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            for (int m = 0; m < TM; ++m) {
+                acc[n][m] = (f32x16)(0.0f);
+                asm volatile("" : "+a"(acc[n][m]));
             }
-        constexpr int kStores = 32 * kChunks / kWave, kRowsStore = kWave / kChunks;
-        const int c = lane % kChunks;
-        if (full) {
+    }
+    wait_stage<(S - 1) * C::kLoads>();
 #pragma unroll
-            for (int i = 0; i < kStores; ++i) {
-                const int row = i * kRowsStore + lane / kChunks;
-                *reinterpret_cast<Out16*>(y_lane + (m * 32 + i * kRowsStore) * pitch) =
-                    *reinterpret_cast<const Out16*>(mine + row * kRow + ((c ^ row) % kChunks) * 16);
+    for (int i = 0; i < kOps; ++i) {
+        read_scale(i, lds);
+#pragma unroll
+        for (int ks = 0; ks < (WALK ? 1 : NS); ++ks) read(i, ks, lds, ks);
+    }
+
+    // Output: 32 rows and 128 bytes of a row (or 64) at a time and wavefront, through LDS for stores of whole lines.
+    constexpr int kEs = OUT == kBf16 ? 2 : 4, kPartN = OUT == kBf16 && TN > 1 ? 2 : 1, kRow = kPartN * 32 * kEs;
+    constexpr int kChunks = kRow / 16, kStores = 32 * kChunks / kWave, kRowsStore = kWave / kChunks;
+    constexpr int kAllStores = TM * TN / kPartN * kStores;   // of a whole tile
+
+    int buf = 0, refill = S - 1;
+    bool stored = false;   // the tile before was stored by kAllStores stores
+    for (;;) {
+        if constexpr (WALK) {
+            for (int t = 0; t < steps; ++t) {
+                const int next = buf + 1 < S ? buf + 1 : 0;
+                const uint8_t* cur_p = lds + buf * C::kStage;
+                const uint8_t* next_p = lds + next * C::kStage;
+    #pragma unroll
+                for (int i = 0; i < TN; ++i) sw[i] = next_sw[i];
+    #pragma unroll
+                for (int i = 0; i < TM; ++i) sx[i] = next_sx[i];
+                // FIRST: the tile's first products, which are not added to anything
+                auto sub_step = [&](auto ks_, auto first_) {
+                    constexpr int ks = ks_;
+                    constexpr bool FIRST = first_;
+                    if constexpr (ks == FA + 1) {
+                        // every wavefront has read this stage: its refill may begin
+                        if constexpr (ks < NS - 1) wait_reads();
+                        else wait_stage_behind<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma), kAllStores>(stored && t == 0);
+                        next_step();
+                        buffers();
+                        refill = buf;
+                    } else if constexpr (ks == NS - 1) {
+                        wait_stage_behind<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma), kAllStores>(stored && t == 0);
+                    }
+                    constexpr int reads = ks < FA || ks == NS - 1 ? kOps : ks == FA ? (NS - 1 - FA) * kOps : 0;
+                    static_for<C::kMfma>([&](auto j_) {
+                        constexpr int j = j_;
+                        static_for<reads>([&](auto i) {
+                            constexpr int at = reads > C::kMfma ? i * C::kMfma / reads : int(i), set = (ks + 1 + i / kOps) % NS;
+                            if constexpr (at == j) {
+                                read(i % kOps, set, ks == NS - 1 ? next_p : cur_p, set);
+                                if constexpr (ks == NS - 1) read_scale(i, next_p);
+                            }
+                        });
+                        constexpr int slot = ((ks + NS - 1 - FA) % NS) * C::kMfma + j;
+                        static_for<C::kLoads>([&](auto i) {
+                            if constexpr (C::slot(i) == slot) load(i, lds0 + refill * C::kStage);
+                        });
+                        constexpr int n = j / TM, m = j % TM;
+                        acc[n][m] = mfma4<ks>(fw[ks][n], fx[ks][m], FIRST ? (f32x16)(0.0f) : acc[n][m], sw[n], sx[m]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                };
+                if (t == 0) sub_step(std::integral_constant<int, 0>{}, std::true_type{});
+                else sub_step(std::integral_constant<int, 0>{}, std::false_type{});
+                static_for<NS - 1>([&](auto i) { sub_step(std::integral_constant<int, i + 1>{}, std::false_type{}); });
+                buf = next;
             }
         } else {
+            // The operands of step t are in set SET, or on their way there; step t + 1's go into the other one.
+            auto step = [&](auto set_) {
+                constexpr int SET = set_;
+                const int next = buf + 1 < S ? buf + 1 : 0;
+                const uint8_t* next_p = lds + next * C::kStage;
+                // every wavefront has read this stage, and the next one is there
+                wait_stage<(S - 2) * C::kLoads>();
+#pragma unroll
+                for (int i = 0; i < TN; ++i) sw[i] = next_sw[i];
+#pragma unroll
+                for (int i = 0; i < TM; ++i) sx[i] = next_sx[i];
+                next_step();
+                buffers();
+                constexpr int kAll = NS * C::kMfma, kReads = (NS + 1) * kOps;
+                static_for<kAll>([&](auto j_) {
+                    constexpr int j = j_;
+                    static_for<kReads>([&](auto i) {
+                        constexpr int at = kReads > kAll ? i * kAll / kReads : int(i);
+                        if constexpr (at == j) {
+                            if constexpr (i < kOps) read_scale(i, next_p);
+                            else read(i % kOps, (1 - SET) * NS + i / kOps - 1, next_p, i / kOps - 1);
+                        }
+                    });
+                    static_for<C::kLoads>([&](auto i) {
+                        if constexpr (C::slot(i) == j) load(i, lds0 + buf * C::kStage);
+                    });
+                    constexpr int ks = j / C::kMfma, n = j % C::kMfma / TM, m = j % TM;
+                    acc[n][m] = mfma4<ks>(fw[SET * NS + ks][n], fx[SET * NS + ks][m], acc[n][m], sw[n], sx[m]);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                buf = next;
+            };
+            int t = 0;
+            for (; t + 1 < steps; t += 2) {
+                step(std::integral_constant<int, 0>{});
+                step(std::integral_constant<int, 1>{});
+            }
+            if (t < steps) step(std::integral_constant<int, 0>{});
+        }
+
+        // A lane has column m = lane % 32 of each block and rows n = 8 g + 4 (lane / 32) + 0..3.
+        if constexpr (!WALK) wait_stage<0>();   // every stage is free
+        uint8_t* mine = lds + (WALK ? S * C::kStage : 0) + wave * 32 * kRow;
+        int lane = threadIdx.x % kWave;
+        asm volatile("" : "+v"(lane));   // what follows from it is formed here, and takes no registers in the loop
+        const int r = lane % 32, h = lane / 32, c = lane % kChunks;
+        const Gemm4Args b = args_again();
+        if constexpr (WALK) tile = tiles.at(b, number);
+        const int64_t pitch = (OUT == kSums ? (int64_t)sums_pitch(b.N) : b.ld_y) * kEs;
+        const bool full = tile.rows_m == BM && tile.rows_n == BN;
+        uint8_t* out = reinterpret_cast<uint8_t*>(OUT == kSums ? b.work : b.y);
+        if (OUT == kSums) out += (int64_t)tile.split * b.M * pitch;
+        uint8_t* y = out + ((int64_t)tile.m0 + wm * C::kRowsM) * pitch + ((int64_t)tile.n0 + wn * C::kRowsN) * kEs;
+        uint8_t* y_lane = y + (lane / kChunks) * pitch + c * 16;
+        auto from = [&](int row) { return mine + row * kRow + (c ^ (row / (256 / kRow) % kChunks)) * 16; };
+        // Of a whole tile, a part is stored only when the next one has been written to LDS: the reads of a part are then
+        // done, and LDS keeps a wavefront's reads before its later writes.
+        constexpr int kParts = TM * TN / kPartN;
+        u32x4 held[kStores];
+        auto store = [&](int part) {
+            const int m = part / (TN / kPartN), n0 = part % (TN / kPartN) * kPartN;
+            uint8_t* to = y_lane + m * 32 * pitch + n0 * 32 * kEs;
+            asm volatile("" : "+v"(to));   // formed here: kept for every store of a tile, addresses need scratch memory
+#pragma unroll
+            for (int i = 0; i < kStores; ++i, to += kRowsStore * pitch)
+                *reinterpret_cast<Out16*>(to) = Out16{{held[i][0], held[i][1], held[i][2], held[i][3]}};
+        };
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+            const int m = part / (TN / kPartN), n0 = part % (TN / kPartN) * kPartN;
+            // (the compiler would convert everything before the first store, which needs scratch memory)
+#pragma unroll
+            for (int n = 0; n < kPartN; ++n) asm volatile("" : "+a"(acc[n0 + n][m]) : : "memory");
+#pragma unroll
+            for (int n = 0; n < kPartN; ++n)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int byte = (n * 32 + 8 * g + 4 * h) * kEs;
+                    uint8_t* p = mine + r * kRow + ((byte / 16) ^ (r / (256 / kRow) % kChunks)) * 16 + byte % 16;
+                    const f32x16& v = acc[n0 + n][m];
+                    if constexpr (OUT == kBf16)
+                        *reinterpret_cast<uint2*>(p) =
+                            make_uint2(bf16_pair(v[4 * g], v[4 * g + 1]), bf16_pair(v[4 * g + 2], v[4 * g + 3]));
+                    else
+                        *reinterpret_cast<float4*>(p) = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+                }
+            if (full) {
+                if (part > 0) store(part - 1);
+#pragma unroll
+                for (int i = 0; i < kStores; ++i)
+                    held[i] = *reinterpret_cast<const u32x4*>(from(i * kRowsStore + lane / kChunks));
+                if (part + 1 == kParts) store(part);
+            } else {
 #pragma unroll 1
-            for (int i = 0; i < kStores; ++i) {
-                const int row = i * kRowsStore + lane / kChunks;
-                const int left_n = rows_n - wn * C::kRowsN - c * (16 / kEs);
-                const uint8_t* p = mine + row * kRow + ((c ^ row) % kChunks) * 16;
-                uint8_t* to = y_lane + (m * 32 + i * kRowsStore) * pitch;
-                if (wm * C::kRowsM + m * 32 + row >= rows_m || left_n <= 0) continue;
-                if (left_n >= 16 / kEs) {
-                    *reinterpret_cast<Out16*>(to) = *reinterpret_cast<const Out16*>(p);
-                } else {
-                    for (int e = 0; e < left_n; ++e) {
-                        if constexpr (OUT == kBf16)
-                            reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(p)[e];
-                        else
-                            reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(p)[e];
+                for (int i = 0; i < kStores; ++i) {
+                    const int row = i * kRowsStore + lane / kChunks;
+                    const int left_n = tile.rows_n - wn * C::kRowsN - n0 * 32 - c * (16 / kEs);
+                    const uint8_t* p = from(row);
+                    uint8_t* to = y_lane + (m * 32 + i * kRowsStore) * pitch + n0 * 32 * kEs;
+                    if (wm * C::kRowsM + m * 32 + row >= tile.rows_m || left_n <= 0) continue;
+                    if (left_n >= 16 / kEs) {
+                        *reinterpret_cast<Out16*>(to) = *reinterpret_cast<const Out16*>(p);
+                    } else {
+                        for (int e = 0; e < left_n; ++e) {
+                            if constexpr (OUT == kBf16)
+                                reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(p)[e];
+                            else
+                                reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(p)[e];
+                        }
                     }
                 }
             }
         }
+        if constexpr (!WALK) return;
+        stored = full;
+        number += gridDim.x;
+        if (number >= tiles.count) return;
     }
 }
 
@@ -391,20 +557,31 @@ __global__ __launch_bounds__(256) void k_gemm4_join(Gemm4Args a, int splits) {
 template <int BM, int BN, int WM, int S, int SP, int FA, int OUT, bool GROUPED>
 hipError_t launch_tile_kernel(const Gemm4Args& a, int tiles_m, int tiles_n, int splits, hipStream_t st) {
     using C = TileCfg<BM, BN, WM, S, SP, FA>;
-    auto kernel = k_gemm4<BM, BN, WM, S, SP, FA, OUT, GROUPED>;
+    // the walk's output goes through LDS of its own (4 KiB a wavefront)
+    constexpr int kOut = 16384;
+    constexpr bool WALK = BM * BN == 256 * 256;
+    constexpr int kLds = C::kLds + (WALK ? kOut : 0);
+    auto kernel = k_gemm4<BM, BN, WM, S, SP, FA, OUT, GROUPED, WALK>;
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_big_lds(kernel, C::kLds, done);
+    const hipError_t e = allow_big_lds(kernel, kLds, done);
     if (e != hipSuccess) return e;
-    return launch_kernel(kernel, dim3((unsigned)(tiles_m * tiles_n * splits)), 256, C::kLds, st, a, tiles_m, tiles_n,
+    const int count = tiles_m * tiles_n * splits;
+    return launch_kernel(kernel, dim3((unsigned)(WALK && count > kCus ? kCus : count)), 256, kLds, st, a, tiles_m, tiles_n,
                          splits);
 }
 
 template <int BM, int BN, int WM, int S, int SP, int FA>
-hipError_t launch_tiles(const Gemm4Args& a, int splits, hipStream_t st) {
+hipError_t launch_tiles(const Gemm4Args& a, hipStream_t st) {
     const int tiles_m = (int)(((int64_t)a.M + BM - 1) / BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
-    if (splits == 1)
-        return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, FA, kBf16, false>(a, tiles_m, tiles_n, 1, st)
-                        : launch_tile_kernel<BM, BN, WM, S, SP, FA, kF32, false>(a, tiles_m, tiles_n, 1, st);
+    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, FA, kBf16, false>(a, tiles_m, tiles_n, 1, st)
+                    : launch_tile_kernel<BM, BN, WM, S, SP, FA, kF32, false>(a, tiles_m, tiles_n, 1, st);
+}
+
+// The same, or with k in parts and their join.
+template <int BM, int BN, int WM, int S, int SP, int FA>
+hipError_t launch_tiles_or_parts(const Gemm4Args& a, int splits, hipStream_t st) {
+    if (splits == 1) return launch_tiles<BM, BN, WM, S, SP, FA>(a, st);
+    const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
     const hipError_t e = launch_tile_kernel<BM, BN, WM, S, SP, FA, kSums, false>(a, tiles_m, tiles_n, splits, st);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)(((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256));
@@ -437,11 +614,14 @@ __global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows,
     static_assert(S * kLoads < 64);   // vmcnt counts to 63
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    int tile_n = blockIdx.x, expert = 0, m0 = 0, m_end = a.M;
-    if constexpr (GROUPED) {
-        if (!group_tile(a, XL * 8, blockIdx.x, tiles_m, tiles_n, expert, m0, m_end, tile_n)) return;
+    Tile tile{0, a.M, (int)blockIdx.x * rows, 0, 0, 0};
+    if constexpr (GROUPED) {   // (`rows` is 32)
+        Tiles<XL * 8, 32, true> tiles(a, tiles_m, tiles_n, 1);
+        if ((int)blockIdx.x >= tiles.count) return;
+        tile = tiles.at(a, blockIdx.x);
     }
-    const int n0 = tile_n * rows, rows_n = a.N - n0 < rows ? a.N - n0 : rows, rows_m = m_end - m0;
+    const int m0 = tile.m0, rows_m = tile.rows_m, expert = tile.expert, n0 = tile.n0;
+    const int rows_n = a.N - n0 < rows ? a.N - n0 : rows;
     const int u0 = a.groups * wave / W, u1 = a.groups * (wave + 1) / W;
     const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds + wave * S * kUnit;
     const uint8_t* ring_p = lds + wave * S * kUnit;
@@ -561,6 +741,7 @@ __global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows,
     }
 }
 
+// (of rows in groups, 32 weight rows a workgroup)
 template <int W, int S, int XL, int OUT, bool GROUPED>
 hipError_t launch_thin_kernel(const Gemm4Args& a, int rows, hipStream_t st) {
     using C = ThinCfg<W, S, XL>;
@@ -591,12 +772,12 @@ size_t gemm4_workspace(int M, int N, int groups) {
 hipError_t launch_gemm4(const Gemm4Args& a, hipStream_t st) {
     const Plan4 p = plan4(a.M, a.N, a.groups);
     switch (p.tile) {
-    case 0: return launch_tiles<256, 256, 2, 2, 48, 0>(a, p.splits, st);
-    case 1: return launch_tiles<128, 256, 2, 3, 32, 0>(a, p.splits, st);
-    case 2: return launch_tiles<128, 128, 2, 4, 16, 0>(a, p.splits, st);
-    case 3: return launch_tiles<64, 256, 1, 3, 16, 0>(a, p.splits, st);
-    case 4: return launch_tiles<32, 256, 1, 4, 8, 0>(a, p.splits, st);
-    case 5: return launch_tiles<64, 64, 2, 8, 4, 0>(a, p.splits, st);
+    case 0: return launch_tiles<256, 256, 2, 2, 48, 0>(a, st);
+    case 1: return launch_tiles_or_parts<128, 256, 2, 3, 32, 0>(a, p.splits, st);
+    case 2: return launch_tiles_or_parts<128, 128, 2, 4, 16, 0>(a, p.splits, st);
+    case 3: return launch_tiles_or_parts<64, 256, 1, 3, 16, 0>(a, p.splits, st);
+    case 4: return launch_tiles_or_parts<32, 256, 1, 4, 8, 0>(a, p.splits, st);
+    case 5: return launch_tiles_or_parts<64, 64, 2, 8, 4, 0>(a, p.splits, st);
     default: return a.y_bf16 ? launch_thin<kBf16>(a, st) : launch_thin<kF32>(a, st);
     }
 }

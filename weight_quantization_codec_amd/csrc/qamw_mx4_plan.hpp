@@ -42,7 +42,7 @@ inline Plan4 plan4(int M, int N, int groups) {
         const int64_t tiles = (((int64_t)M + c.bm - 1) / c.bm) * (((int64_t)N + c.bn - 1) / c.bn);
         if (tiles > kMaxTiles4) continue;   // of 256 x 256 tiles there are never more
         for (const int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            if (s > 1 && (tiles * s > kCus || groups / s < 3)) break;
+            if (s > 1 && (i == 0 || tiles * s > kCus || groups / s < 3)) break;   // the largest tiles gain nothing by it
             const double rounds = (double)((tiles * s + kCus - 1) / kCus), part = (double)((groups + s - 1) / s);
             double t = kLaunch4 + rounds * (c.start + part * c.step);
             if (s > 1) t += kJoin4 + s * m * n * 8 / kJoinTraffic4;
