@@ -181,21 +181,22 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     // wavefront loads codes of (up to) 64 rows and scales of 64: a lane fetches the index of one of either, and the
     // others ask it.
     auto offsets = [&](const Gemm4Args& a, const Tile& at, bool of_x_only) {
-        int lane = threadIdx.x % kWave, of_codes = 0, of_scales = 0;
+        uint32_t lane = threadIdx.x % kWave;
+        int of_codes = 0, of_scales = 0;
         asm volatile("" : "+v"(lane));   // what follows from it is formed here, and takes no registers in the loop
-        auto fetch = [&](int r) { return a.index[at.m0 + (r < at.rows_m ? r : at.rows_m - 1)]; };
+        auto fetch = [&](uint32_t r) { return a.index[at.m0 + ((int)r < at.rows_m ? (int)r : at.rows_m - 1)]; };
         if (indexed) {
             of_codes = fetch((lane / 8 * 4 + wave) * 8 + lane % 8);
             of_scales = fetch((lane / 32 * 4 + wave) * 32 + lane % 32);
         }
-        auto far = [&](int r, int row) { return r >= at.rows_m || row < 0 || row >= a.x_rows; };
+        auto far = [&](uint32_t r, int row) { return (int)r >= at.rows_m || row < 0 || row >= a.x_rows; };
 #pragma unroll
         for (int i = 0; i < C::kScaleLoads; ++i) {
             const int n = i * 4 + wave, part = n < C::kScaleRows ? n : C::kScaleRows - 1;
             const bool is_x = kLoadsX % 4 ? part < kLoadsX : i < kLoadsX / 4;
             if (of_x_only && !is_x) continue;
-            const int r = (is_x ? part : part - kLoadsX) * 32 + lane / 2;
-            voff[i] = (uint32_t)r * 8 + lane % 2 * 4;
+            const uint32_t r = (uint32_t)(is_x ? part : part - kLoadsX) * 32 + lane / 2;
+            voff[i] = r * 8 + lane % 2 * 4;
             if (indexed && is_x) {
                 const int row = __shfl(of_scales, i * 32 % kWave + lane / 2);
                 voff[i] = far(r, row) ? kFar : (uint32_t)row * 8 + lane % 2 * 4;
@@ -205,10 +206,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
         for (int i = 0; i < C::kCodeLoads; ++i) {
             const bool is_x = i < kLoadsX;
             if (of_x_only && !is_x) continue;
-            const int r = ((is_x ? i : i - kLoadsX) * 4 + wave) * 8 + lane / 8;
-            const uint32_t chunk = (uint32_t)((lane % 8) ^ (r / 2 % 8)) * 16;
+            const uint32_t r = (uint32_t)((is_x ? i : i - kLoadsX) * 4 + wave) * 8 + lane / 8;
+            const uint32_t chunk = ((lane % 8) ^ (r / 2 % 8)) * 16;
             uint32_t& v = voff[C::kScaleLoads + i];
-            v = (uint32_t)r * (uint32_t)(is_x ? a.ld_x : a.ld_w) + chunk;
+            v = r * (uint32_t)(is_x ? a.ld_x : a.ld_w) + chunk;
             if (indexed && is_x) {
                 const int row = __shfl(of_codes, i * 8 % kWave + lane / 8);
                 v = far(r, row) ? kFar : (uint32_t)row * (uint32_t)a.ld_x + chunk;
@@ -438,10 +439,17 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
 
         // A lane has column m = lane % 32 of each block and rows n = 8 g + 4 (lane / 32) + 0..3.
         if constexpr (!WALK) wait_stage<0>();   // every stage is free
-        uint8_t* mine = lds + (WALK ? S * C::kStage : 0) + wave * 32 * kRow;
-        int lane = threadIdx.x % kWave;
+        uint32_t lane = threadIdx.x % kWave;
         asm volatile("" : "+v"(lane));   // what follows from it is formed here, and takes no registers in the loop
-        const int r = lane % 32, h = lane / 32, c = lane % kChunks;
+        const uint32_t r = lane % 32, h = lane / 32 % 2, c = lane % kChunks, row = lane / kChunks % kRowsStore;
+        // LDS row q holds its 16-byte chunk j at place j ^ turn(q), so that 16 rows' chunks j are in different banks.
+        // Rows and places are different bits of an address: one exclusive or goes from one to the next.
+        auto turn = [](uint32_t q) { return q / (256 / kRow) % kChunks; };
+        uint8_t* mine = lds + (WALK ? S * C::kStage : 0) + wave * 32 * kRow;
+        const uint32_t mine0 = (uint32_t)(mine - lds);
+        const uint32_t to0 = mine0 + r * kRow + ((4 * h * kEs / 16) ^ turn(r)) * 16 + 4 * h * kEs % 16;
+        const uint32_t from0 = mine0 + row * kRow + (c ^ turn(row)) * 16;
+        auto from = [&](int i) { return lds + ((from0 ^ (turn(i * kRowsStore) * 16)) + i * kRowsStore * kRow); };
         const Gemm4Args b = args_again();
         if constexpr (WALK) tile = tiles.at(b, number);
         const int64_t pitch = (OUT == kSums ? (int64_t)sums_pitch(b.N) : b.ld_y) * kEs;
@@ -449,8 +457,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
         uint8_t* out = reinterpret_cast<uint8_t*>(OUT == kSums ? b.work : b.y);
         if (OUT == kSums) out += (int64_t)tile.split * b.M * pitch;
         uint8_t* y = out + ((int64_t)tile.m0 + wm * C::kRowsM) * pitch + ((int64_t)tile.n0 + wn * C::kRowsN) * kEs;
-        uint8_t* y_lane = y + (lane / kChunks) * pitch + c * 16;
-        auto from = [&](int row) { return mine + row * kRow + (c ^ (row / (256 / kRow) % kChunks)) * 16; };
+        uint8_t* y_lane = y + row * pitch + c * 16;
         // Of a whole tile, a part is stored only when the next one has been written to LDS: the reads of a part are then
         // done, and LDS keeps a wavefront's reads before its later writes.
         constexpr int kParts = TM * TN / kPartN;
@@ -473,8 +480,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
             for (int n = 0; n < kPartN; ++n)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int byte = (n * 32 + 8 * g + 4 * h) * kEs;
-                    uint8_t* p = mine + r * kRow + ((byte / 16) ^ (r / (256 / kRow) % kChunks)) * 16 + byte % 16;
+                    uint8_t* p = lds + (to0 ^ ((n * 32 + 8 * g) * kEs));
                     const f32x16& v = acc[n0 + n][m];
                     if constexpr (OUT == kBf16)
                         *reinterpret_cast<uint2*>(p) =
@@ -486,16 +492,16 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
                 if (part > 0) store(part - 1);
 #pragma unroll
                 for (int i = 0; i < kStores; ++i)
-                    held[i] = *reinterpret_cast<const u32x4*>(from(i * kRowsStore + lane / kChunks));
+                    held[i] = *reinterpret_cast<const u32x4*>(from(i));
                 if (part + 1 == kParts) store(part);
             } else {
 #pragma unroll 1
                 for (int i = 0; i < kStores; ++i) {
-                    const int row = i * kRowsStore + lane / kChunks;
-                    const int left_n = tile.rows_n - wn * C::kRowsN - n0 * 32 - c * (16 / kEs);
-                    const uint8_t* p = from(row);
+                    const int left_m = tile.rows_m - wm * C::kRowsM - m * 32 - i * kRowsStore - (int)row;
+                    const int left_n = tile.rows_n - wn * C::kRowsN - n0 * 32 - (int)c * (16 / kEs);
+                    const uint8_t* p = from(i);
                     uint8_t* to = y_lane + (m * 32 + i * kRowsStore) * pitch + n0 * 32 * kEs;
-                    if (wm * C::kRowsM + m * 32 + row >= tile.rows_m || left_n <= 0) continue;
+                    if (left_m <= 0 || left_n <= 0) continue;
                     if (left_n >= 16 / kEs) {
                         *reinterpret_cast<Out16*>(to) = *reinterpret_cast<const Out16*>(p);
                     } else {
@@ -761,6 +767,13 @@ hipError_t launch_thin(const Gemm4Args& a, hipStream_t st) {
     return launch_thin_kernel<4, 2, 4, OUT, false>(a, rows, st);
 }
 
+// 8 XL rows of a group at a time.
+template <int XL>
+hipError_t launch_group_thin(const Gemm4Args& a, hipStream_t st) {
+    return a.y_bf16 ? launch_thin_kernel<4, 2, XL, kBf16, true>(a, 32, st)
+                    : launch_thin_kernel<4, 2, XL, kF32, true>(a, 32, st);
+}
+
 }  // namespace
 
 size_t gemm4_workspace(int M, int N, int groups) {
@@ -774,22 +787,22 @@ hipError_t launch_gemm4(const Gemm4Args& a, hipStream_t st) {
     switch (p.tile) {
     case 0: return launch_tiles<256, 256, 2, 2, 48, 0>(a, st);
     case 1: return launch_tiles_or_parts<128, 256, 2, 3, 32, 0>(a, p.splits, st);
-    case 2: return launch_tiles_or_parts<128, 128, 2, 4, 16, 0>(a, p.splits, st);
+    case 2: return launch_tiles_or_parts<128, 128, 2, 3, 16, 0>(a, p.splits, st);
     case 3: return launch_tiles_or_parts<64, 256, 1, 3, 16, 0>(a, p.splits, st);
     case 4: return launch_tiles_or_parts<32, 256, 1, 4, 8, 0>(a, p.splits, st);
-    case 5: return launch_tiles_or_parts<64, 64, 2, 8, 4, 0>(a, p.splits, st);
+    case 5: return launch_tiles_or_parts<64, 64, 2, 4, 4, 0>(a, p.splits, st);
     default: return a.y_bf16 ? launch_thin<kBf16>(a, st) : launch_thin<kF32>(a, st);
     }
 }
 
 hipError_t launch_gemm4_grouped(const Gemm4Args& a, hipStream_t st) {
-    switch (plan4_grouped(a.M, a.experts, a.N)) {
+    switch (plan4_grouped(a.M, a.experts, a.N, a.groups)) {
     case 0: return launch_group_tiles<256, 256, 2, 2, 48, 0>(a, st);
     case 1: return launch_group_tiles<128, 256, 2, 3, 32, 0>(a, st);
     case 3: return launch_group_tiles<64, 256, 1, 3, 16, 0>(a, st);
     case 4: return launch_group_tiles<32, 256, 1, 4, 8, 0>(a, st);
-    default: return a.y_bf16 ? launch_thin_kernel<4, 2, 1, kBf16, true>(a, 32, st)
-                             : launch_thin_kernel<4, 2, 1, kF32, true>(a, 32, st);
+    case kThin4: return launch_group_thin<1>(a, st);
+    default: return launch_group_thin<2>(a, st);
     }
 }
 
