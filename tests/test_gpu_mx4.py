@@ -65,7 +65,7 @@ def _same(got, want):
 
 
 SHAPES = [(1, 1), (3, 7), (2, 31), (5, 32), (4, 33), (6, 255), (1, 256), (33, 257), (7, 1003), (1, 5120), (300, 4100),
-          (5, 13824), (2, 40000), (700, 64), (4099, 300)]
+          (5, 13824), (2, 40000), (700, 64), (4099, 300), (20000, 40), (9000, 300), (7001, 5), (12000, 17), (3000, 1003)]
 TYPES = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 
 
@@ -103,7 +103,7 @@ def test_quant4_and_back(q, n, d, dtype):
 
 @TYPES
 @pytest.mark.parametrize("with_scale", [False, True])
-@pytest.mark.parametrize("n,d", [(1, 1), (5, 17), (64, 1003), (3, 5120), (9, 13824), (700, 300)])
+@pytest.mark.parametrize("n,d", [(1, 1), (5, 17), (64, 1003), (3, 5120), (9, 13824), (700, 300), (9000, 75)])
 def test_quant4_gated(q, n, d, with_scale, dtype):
     """Gate and up as the halves of one matrix.  A gated value is within 2^-38 of itself before it is rounded to
     fp32: the roundings of both ends of that range have to give the codes, block by block."""
@@ -235,7 +235,7 @@ def _check_norm(room, forms, n):
 
 @TYPES
 @pytest.mark.parametrize("n,d", [(1, 1), (3, 7), (2, 33), (5, 256), (4, 257), (33, 513), (7, 1003), (1, 4096), (300, 4100),
-                                 (1100, 5120), (3, 8200), (2, 13824), (3, 16400), (2, 24576), (2, 32768), (2050, 640)])
+                                 (1100, 5120), (3, 8200), (2, 13824), (3, 16400), (2, 24576), (2, 32768), (2050, 640), (5000, 43)])
 def test_rmsnorm4(q, n, d, dtype):
     rng = np.random.default_rng(n * 7919 + d)
     pad, offset, extra = [(0, 0, 0), (5, 3, 16), (d % 3, 1, 0)][(n + d) % 3]
@@ -299,12 +299,20 @@ def test_rmsnorm4_special_rows(q):
 # ---------------------------------------------------------------- products
 
 def _form(q, rng, n, d, spread=0, extra=0):
-    """Codes and scales of n x d values on the device (scales over `spread` binades more), and the values."""
-    a = rng.standard_normal((n, d)).astype(np.float32)
-    if spread:
-        b = ref.blocks(a)
-        a = (b * np.exp2(rng.integers(-spread, spread + 1, b.shape[:2] + (1,)))).astype(np.float32).reshape(n, -1)[:, :d]
-    c, s = ref.quantize(a)
+    """Codes and scales of n x d values on the device (scales over `spread` binades more), and the values.  Of many
+    values, codes drawn as such."""
+    if n * d <= 300000:
+        a = rng.standard_normal((n, d)).astype(np.float32)
+        if spread:
+            b = ref.blocks(a)
+            a = (b * np.exp2(rng.integers(-spread, spread + 1, b.shape[:2] + (1,)))).astype(np.float32).reshape(n, -1)[:, :d]
+        c, s = ref.quantize(a)
+    else:
+        c = rng.integers(0, 256, (n, q.mx4_stride(d)), dtype=np.uint8)
+        s = rng.integers(125 - spread, 128 + spread, (q.mx4_groups(d), n, 8), dtype=np.uint8)
+        c[:, (d + 1) // 2:] = 0
+        if d % 2:
+            c[:, d // 2] &= 15
     room = _room(q, n, d, extra)
     room[2].copy_(torch.from_numpy(c).to(DEV))
     room[3].copy_(torch.from_numpy(s).to(DEV))
@@ -362,9 +370,20 @@ def test_gemm4_scales_of_any_size(q, M, N, K):
     _product(q, M, N, K, seed=1, spread=20)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 5120, 5120), (16, 13824, 5120), (77, 4096, 11008), (515, 5120, 4096), (1500, 5120, 5120),
-                                   (2100, 4100, 1100)])
-def test_gemm4_large(q, M, N, K):
+# Sizes that go to each of the kernels, in the order of their choice (test_mx4_plan.py asserts that they do): tiles of 256
+# x 256, one tile a workgroup and several, with one group of columns and more; 128 x 256; 128 x 128, k whole and in
+# parts; 64 x 256; 32 x 256; 64 x 64; few rows, of each width.
+KERNELS = [(857, 9539, 256), (2300, 4500, 200), (5000, 5000, 100), (5000, 5700, 700), (2049, 4100, 1200),
+           (979, 5570, 256), (1300, 5300, 700), (1500, 5120, 5120),
+           (131, 13841, 256), (515, 5120, 4096), (68, 5633, 12200), (2609, 747, 13200), (102, 2956, 13500),
+           (130, 13121, 256), (276, 6348, 14800), (39, 10656, 13300), (47, 6050, 13500),
+           (132, 11089, 256), (17, 13779, 11500), (91, 2881, 10400),
+           (33, 16, 256), (77, 4096, 11008), (33, 4139, 6000), (51, 2111, 5500), (80, 158, 11400), (600, 2049, 700),
+           (1, 5120, 5120), (8, 300, 1000), (9, 4096, 4000), (16, 13824, 5120), (17, 5120, 5000), (32, 333, 1700)]
+
+
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_gemm4_every_kernel(q, M, N, K):
     _product(q, M, N, K)
 
 
@@ -460,10 +479,20 @@ def test_grouped_rows_without_a_group(q):
     _grouped(q, 300, [100, 70], 200, 300, False, first=70, behind=60)
 
 
-@pytest.mark.parametrize("x_rows,sizes,N,K", [(24, [3] * 32, 4096, 4096), (515, [700, 0, 100, 230], 1024, 2048),
-                                              (1000, [37, 500, 1, 462], 5120, 1100), (2048, [300] * 12, 768, 512)])
-def test_grouped_large(q, x_rows, sizes, N, K):
+# The same for rows in groups: 256 x 256 (one tile a workgroup and several, more than 64 groups), 128 x 256, 64 x 256,
+# 32 x 256, few rows.
+GROUP_KERNELS = [(3000, [2000, 3074, 600], 5200, 256), (700, [3000, 3074, 600], 5200, 600), (2000, [9, 20000] + [0] * 63 + [19991], 1500, 200),
+                 (1000, [37, 500, 1, 462], 5120, 1100), (5000, [60] * 80 + [900], 500, 300),
+                 (400, [40] * 90 + [333, 7], 1024, 1800), (700, [300, 90, 610, 200], 1700, 256),
+                 (515, [700, 0, 100, 230], 1024, 2048), (64, [33, 31], 5120, 5000),
+                 (24, [3] * 31 + [40], 512, 4096), (70, [1] * 70, 40, 512), (100, [50, 0, 17, 133], 300, 900)]
+
+
+@pytest.mark.parametrize("x_rows,sizes,N,K", GROUP_KERNELS)
+def test_grouped_every_kernel(q, x_rows, sizes, N, K):
     _grouped(q, x_rows, sizes, N, K, True)
+    if sum(sizes) < 4000:
+        _grouped(q, sum(sizes), sizes, N, K, False, seed=1)
 
 
 def test_grouped_equals_products(q):

@@ -174,36 +174,39 @@ __global__ __launch_bounds__(256) void k_quant4(Rows4Args a, int tx, int rows_wg
         flag |= bad;
         store_codes(a, row, c, q, s);
     };
+    // The lanes of a block, and the 16 of a store, exchange values: whatever a lane has of the row, it comes to `write`
+    // with the others.  One without a whole chunk loads the last whole one instead, and then what it has.
+    const int whole = a.d / kChunk, at_j = (c < whole ? c : whole > 0 ? whole - 1 : 0) * kChunk;
+    auto load = [&](int64_t row, Raw<BF>& x, Raw<BF>& o) {
+        x = *reinterpret_cast<const Raw<BF>*>(at<BF>(a.x, row * a.ld_x + at_j));
+        if constexpr (GATE) o = *reinterpret_cast<const Raw<BF>*>(at<BF>(a.other, row * a.ld_other + at_j));
+    };
+    auto take = [&](int64_t row, const Raw<BF>& x, const Raw<BF>& o) {
+        float v[kChunk], g[kChunk];
+        unpack<BF>(x, v);
+        if constexpr (GATE) unpack<BF>(o, g);
+        if (have < kChunk) {
+            load_part<BF>(at<BF>(a.x, row * a.ld_x + j), have, v);
+            if constexpr (GATE) load_part<BF>(at<BF>(a.other, row * a.ld_other + j), have, g);
+        }
+        write(row, v, g);
+    };
     int64_t row = first + threadIdx.x / tx;
-    if (have >= kChunk) {
+    if (whole > 0) {
         // four rows at a time, every load under way before the first is used
         constexpr int U = 4;
         for (; row + (U - 1) * ty < end; row += U * ty) {
             Raw<BF> x[U], o[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                x[u] = *reinterpret_cast<const Raw<BF>*>(at<BF>(a.x, (row + u * ty) * a.ld_x + j));
-                if constexpr (GATE) o[u] = *reinterpret_cast<const Raw<BF>*>(at<BF>(a.other, (row + u * ty) * a.ld_other + j));
-            }
+            for (int u = 0; u < U; ++u) load(row + u * ty, x[u], o[u]);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float v[kChunk], g[kChunk];
-                unpack<BF>(x[u], v);
-                if constexpr (GATE) unpack<BF>(o[u], g);
-                write(row + u * ty, v, g);
-            }
+            for (int u = 0; u < U; ++u) take(row + u * ty, x[u], o[u]);
         }
     }
     for (; row < end; row += ty) {
-        float v[kChunk], g[kChunk];
-        if (have >= kChunk) {
-            unpack<BF>(*reinterpret_cast<const Raw<BF>*>(at<BF>(a.x, row * a.ld_x + j)), v);
-            if constexpr (GATE) unpack<BF>(*reinterpret_cast<const Raw<BF>*>(at<BF>(a.other, row * a.ld_other + j)), g);
-        } else {
-            load_part<BF>(at<BF>(a.x, row * a.ld_x + j), have, v);
-            if constexpr (GATE) load_part<BF>(at<BF>(a.other, row * a.ld_other + j), have, g);
-        }
-        write(row, v, g);
+        Raw<BF> x{}, o{};
+        if (whole > 0) load(row, x, o);
+        take(row, x, o);
     }
     if (flag && a.status) atomicOr(a.status, QAMW_FLAG_NONFINITE);
 }
