@@ -66,7 +66,7 @@ def build_host() -> str:
     cmd += [os.path.join(CSRC, "w8_host.cpp"), os.path.join(CSRC, "mx4_host.cpp"), "-o", tmp]
     for d in cpp_extension.library_paths():
         cmd += ["-L", d]
-    cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    cmd += ["-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip"]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
         failure = r.stderr[-4000:] if r.returncode else None

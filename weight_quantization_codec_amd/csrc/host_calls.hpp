@@ -5,6 +5,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
+#include <ATen/hip/impl/HIPCachingAllocatorMasqueradingAsCUDA.h>
 #include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -72,8 +74,11 @@ inline void* stream(int device) { return c10::hip::getCurrentHIPStream((c10::Dev
 
 inline qamw_dtype dtype(const Tensor& t) { return t.scalar_type() == at::kBFloat16 ? QAMW_BF16 : QAMW_F32; }
 
-inline Tensor make(const Tensor& like, at::IntArrayRef size, at::ScalarType type) {
-    return at::empty(size, like.options().dtype(type).requires_grad(false));
+// An output on the current device, as at::empty makes it at the end of its way through the dispatcher; that way takes
+// as long again (quant4 of a row, calls one behind the other: 4.8 us with it, 4.1 without).
+inline Tensor make(at::IntArrayRef size, at::ScalarType type) {
+    return at::detail::empty_generic(size, c10::hip::HIPCachingAllocatorMasqueradingAsCUDA::get(),
+                                     c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
 // A tuple of new references; null if one of them is.

@@ -1,8 +1,8 @@
 // The ordinary calls of the 4-bit operators, without the interpreter between their checks, as w8_host.cpp has those of
 // the 8-bit ones: a function here returns None for every other call, before anything is queued, and mx4.py does it.
 //
-// Calls one behind the other, one row (us): see the table of the design notes' host section for the 8-bit ones; these
-// take as long.
+// Calls one behind the other, one row (us, in the interpreter and here): quant4 8.4 and 4.1, dequant4 7.4 and 3.6,
+// rmsnorm4 with a residual 11 and 4.7, gemm4 10 and 4.4.
 #include "host_calls.hpp"
 #include "qamw_mx4.h"
 
@@ -51,9 +51,9 @@ const int32_t* ints(const Tensor& t, int device, int64_t n) {
     return t.const_data_ptr<int32_t>();
 }
 
-void make_form(const Tensor& like, int64_t n, int64_t d, Tensor& q, Tensor& e) {
-    q = make(like, {n, 128 * groups_of(d)}, at::kByte);
-    e = make(like, {groups_of(d), n, 8}, at::kByte);
+void make_form(int64_t n, int64_t d, Tensor& q, Tensor& e) {
+    q = make({n, 128 * groups_of(d)}, at::kByte);
+    e = make({groups_of(d), n, 8}, at::kByte);
 }
 
 PyObject* quant4(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -68,7 +68,7 @@ PyObject* quant4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            make_form(x, r.n, r.d, q, e);
+            make_form(r.n, r.d, q, e);
             rc = lib.quant4(r.p, dtype(x), r.n, r.d, r.ld, g.p, g.ld, scale, q.data_ptr<uint8_t>(), q.size(1),
                             e.data_ptr<uint8_t>(), 8ll * r.n, nullptr, stream(dev));
         }
@@ -91,7 +91,7 @@ PyObject* dequant4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            y = make(q, {f.n, d}, a[4] == Py_True ? at::kBFloat16 : at::kFloat);
+            y = make({f.n, d}, a[4] == Py_True ? at::kBFloat16 : at::kFloat);
             rc = lib.dequant4(f.q, f.n, (int32_t)d, f.ld_q, f.e, f.ld_e, scale, y.data_ptr(), dtype(y), d, stream(dev));
         }
         check(rc, "qamw_dequant4");
@@ -120,8 +120,8 @@ PyObject* rmsnorm4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            if (o.p) h = make(x, {r.n, r.d}, x.scalar_type());
-            make_form(x, r.n, r.d, q, e);
+            if (o.p) h = make({r.n, r.d}, x.scalar_type());
+            make_form(r.n, r.d, q, e);
             rc = lib.rmsnorm4(r.p, dtype(x), r.n, r.d, r.ld, o.p, o.ld, w, (float)eps, o.p ? h.data_ptr() : nullptr,
                               r.d, q.data_ptr<uint8_t>(), q.size(1), e.data_ptr<uint8_t>(), 8ll * r.n, nullptr, stream(dev));
         }
@@ -141,9 +141,9 @@ PyObject* gemm4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            y = make(xq, {x.n, w.n}, a[4] == Py_True ? at::kBFloat16 : at::kFloat);
+            y = make({x.n, w.n}, a[4] == Py_True ? at::kBFloat16 : at::kFloat);
             const size_t need = lib.gemm4_workspace(x.n, w.n, x.groups);
-            if (need) work = make(xq, {(int64_t)need}, at::kByte);
+            if (need) work = make({(int64_t)need}, at::kByte);
             rc = lib.gemm4(x.q, x.ld_q, x.e, x.ld_e, x.n, w.q, w.ld_q, w.e, w.ld_e, w.n, x.groups, y.data_ptr(), dtype(y),
                            w.n, need ? work.data_ptr() : nullptr, need, stream(dev));
         }
@@ -186,7 +186,7 @@ PyObject* gemm4_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            y = make(xq, {many, N}, a[6] == Py_True ? at::kBFloat16 : at::kFloat);
+            y = make({many, N}, a[6] == Py_True ? at::kBFloat16 : at::kFloat);
             rc = lib.gemm4_grouped(x.q, x.ld_q, x.e, x.ld_e, x.n, index, (int32_t)many, pw, ld_w, by, pe, ld_we, eby,
                                    offsets, (int32_t)E, (int32_t)N, x.groups, y.data_ptr(), dtype(y), N, stream(dev));
         }

@@ -40,9 +40,9 @@ Rows codes(const Tensor& t, int device) {
 }
 
 // Codes for n rows of d columns: rows of whole 16-byte chunks.
-Tensor make_codes(const Tensor& like, int64_t n, int64_t d) {
+Tensor make_codes(int64_t n, int64_t d) {
     const int64_t pitch = (d + 15) / 16 * 16;
-    Tensor q = make(like, {n, pitch}, at::kChar);
+    Tensor q = make({n, pitch}, at::kChar);
     return pitch == d ? q : q.slice(1, 0, d);
 }
 
@@ -60,8 +60,8 @@ PyObject* quant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            q = make_codes(x, r.n, r.d);
-            s = make(x, {r.n}, at::kFloat);
+            q = make_codes(r.n, r.d);
+            s = make({r.n}, at::kFloat);
             rc = lib.quant8(r.p, dtype(x), r.n, r.d, r.ld, g.p, g.ld, scale, q.data_ptr<int8_t>(), pitch_of(r.d),
                             s.data_ptr<float>(), nullptr, stream(dev));
         }
@@ -81,7 +81,7 @@ PyObject* dequant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            y = make(c, {r.n, r.d}, a[3] == Py_True ? at::kBFloat16 : at::kFloat);
+            y = make({r.n, r.d}, a[3] == Py_True ? at::kBFloat16 : at::kFloat);
             rc = lib.dequant8((const int8_t*)r.p, r.n, r.d, r.ld, s, scale, y.data_ptr(), dtype(y), r.d, stream(dev));
         }
         check(rc, "qamw_dequant8");
@@ -110,9 +110,9 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            if (o.p) h = make(x, {r.n, r.d}, x.scalar_type());
-            q = make_codes(x, r.n, r.d);
-            s = make(x, {r.n}, at::kFloat);
+            if (o.p) h = make({r.n, r.d}, x.scalar_type());
+            q = make_codes(r.n, r.d);
+            s = make({r.n}, at::kFloat);
             rc = lib.rmsnorm8(r.p, dtype(x), r.n, r.d, r.ld, o.p, o.ld, w, (float)eps, o.p ? h.data_ptr() : nullptr,
                               r.d, q.data_ptr<int8_t>(), pitch_of(r.d), s.data_ptr<float>(), nullptr, stream(dev));
         }
@@ -134,9 +134,9 @@ PyObject* gemm8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int rc;
         {
             const Unlocked unlocked;
-            y = make(xq, {x.n, w.n}, a[4] == Py_True ? at::kBFloat16 : at::kFloat);
+            y = make({x.n, w.n}, a[4] == Py_True ? at::kBFloat16 : at::kFloat);
             const size_t need = lib.gemm8_workspace(x.n, w.n, x.d);
-            if (need) work = make(xq, {(int64_t)need}, at::kByte);
+            if (need) work = make({(int64_t)need}, at::kByte);
             rc = lib.gemm8((const int8_t*)x.p, x.ld, xs, x.n, (const int8_t*)w.p, w.ld, ws, w.n, x.d, y.data_ptr(),
                            dtype(y), w.n, need ? work.data_ptr() : nullptr, need, stream(dev));
         }
