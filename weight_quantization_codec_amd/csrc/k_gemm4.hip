@@ -5,6 +5,16 @@
 // and lanes 0-31 and 32-63 have two different blocks.  Which blocks does not matter as long as both operands agree:
 // of a group of 8 blocks the lower lanes have 0-3 and the upper ones 4-7, so that a lane's four scale bytes are
 // the four bytes of a register, from which the instruction takes the one that it is told.
+//
+// Two kernels.  k_gemm4 forms tiles of y, with the operands in stages of a group of 256 columns in LDS; where the tiles
+// do not fill the chip, k is split over workgroups too and k_gemm4_join adds their sums, in fp32 and in the order of
+// k.  k_gemm4_thin, for few activation rows, is bound by one read of the weights.  Both have a form for rows in groups.
+// plan4() and plan4_grouped() (qamw_mx4_plan.hpp) choose.
+//
+// Loads.  A stage is 128 bytes of codes of every row, whole lines of memory, and 8 bytes of scales, which stand together
+// for the rows of a tile (groups are the outermost dimension of the scales): with scales by rows a stage would fetch
+// 64 bytes of them for every 8.  Everything goes from memory straight to LDS; rows and columns past the end come
+// from the buffer's bounds as zeros, code and scale alike, so there are no masks.
 #include "qamw_device.hpp"
 #include "qamw_mx4_launch.hpp"
 #include "qamw_mx4_plan.hpp"
@@ -112,6 +122,20 @@ enum { kF32 = 0, kBf16 = 1, kSums = 2 };
 
 // A tile of BM activation rows by BN weight rows, WM x 4 / WM wavefronts, S stages of a group of columns in LDS: the
 // rows' 128 bytes of codes, then their 8 bytes of scales.
+//
+// What bounds it.  256 x 256 of a group are 64 matrix instructions of 32 cycles for each of the 4 SIMDs, 2099 cycles, in
+// which LDS delivers 128 KiB to the operands and takes in 68.  At 8192 x 13824 x 5120 a step takes 2880 cycles (2590 with
+// empty buffers, 3070 without the matrix instructions), at 1.65 to 1.75 GHz: the chip's power is the limit, and what
+// moves data takes its part of it.  Matrix instructions from registers alone reach 6.75 PFLOP/s on codes of normal
+// values (9.2 on zeros, at 2.3 GHz); here 4.0 to 4.25.  Smaller tiles have fewer matrix cycles for the bytes that LDS
+// moves: a step of 128 x 128 is 525 matrix cycles and 770 of LDS, and takes 870 with empty buffers.
+//   step by step (us, that size): operands as they stand in memory, no LDS 2557; tiles through LDS, one tile a workgroup
+//   289 (of 70000 cycles a tile 8000 until the first stage is there and 7400 for the output); conversions to bf16 in
+//   pairs 281; workgroups that walk over tiles 276 to 290 on cards where the form before takes 281 to 293 (the cycles
+//   fall by 10%, the clock by 6%).
+//   Not kept: the stage's operands read over two or three sub-steps instead of one (FA 1: +1%, FA 2: +12%); a refill
+//   over 32 (+2%) or 60 (-1%, but then a walk's stores stand before loads) instructions; all sums of a part read
+//   before the first conversion (+11%: scratch memory).
 template <int BM, int BN, int WM, int S, int SP, int FA>
 struct TileCfg {
     static constexpr int kWN = 4 / WM, kRowsM = BM / WM, kRowsN = BN / kWN;   // a wavefront's part
@@ -601,7 +625,9 @@ hipError_t launch_group_tiles(const Gemm4Args& a, hipStream_t st) {
                     : launch_tile_kernel<BM, BN, WM, S, SP, FA, kF32, true>(a, tiles_m, tiles_n, 1, st);
 }
 
-// Few activation rows: bound by the one read of the weights.  A workgroup has up to 32 weight rows and W wavefronts
+// Few activation rows: bound by the one read of the weights (1 x 5120 x 5120: 4.6 us, 3.0 TB/s with a launch in it; 1 x
+// 13824 x 5120: 7.9, 4.8 TB/s; 96 rows in 32 groups, 4096 x 4096: 58, 4.9 TB/s).  A ring of 2 units, 4 wavefronts: with 3
+// units a workgroup fewer fits a compute unit (10% longer in groups), with 8 wavefronts the same (20%).  A workgroup has up to 32 weight rows and W wavefronts
 // that split k between them.  Each wavefront runs on its own: it loads a group of columns of all rows (a unit) at a
 // time into its own ring of S units in LDS (XL loads of 8 activation rows, 4 of weight rows, and their scales), and
 // waits for nothing but its own loads.
