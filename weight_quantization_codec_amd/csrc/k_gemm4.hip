@@ -86,7 +86,8 @@ struct Tiles {
         t.split = tile_of(number, splits, tiles_m, tiles_n, tile_m, tile_n);
         int m_end = a.M;
         if constexpr (GROUPED) {
-            for (int e0 = 0;; e0 += kWave) {
+            m_end = 0;   // (a tile without rows, should the offsets change under the call)
+            for (int e0 = 0; e0 < a.experts; e0 += kWave) {
                 if (a.experts > kWave) g = groups_from(a, BM, e0 + (int)threadIdx.x % kWave);
                 const uint64_t reached = __ballot(g.sum > tile_m);
                 if (reached) {
@@ -133,10 +134,10 @@ enum { kF32 = 0, kBf16 = 1, kSums = 2 };
 //   289 (of 70000 cycles a tile 8000 until the first stage is there and 7400 for the output); conversions to bf16 in
 //   pairs 281; workgroups that walk over tiles 276 to 290 on cards where the form before takes 281 to 293 (the cycles
 //   fall by 10%, the clock by 6%).
-//   Not kept: the stage's operands read over two or three sub-steps instead of one (FA 1: +1%, FA 2: +12%); a refill
+//   Not kept: the stage's operands read over two or three sub-steps instead of one (+1%, +12%); a refill
 //   over 32 (+2%) or 60 (-1%, but then a walk's stores stand before loads) instructions; all sums of a part read
 //   before the first conversion (+11%: scratch memory).
-template <int BM, int BN, int WM, int S, int SP, int FA>
+template <int BM, int BN, int WM, int S, int SP>
 struct TileCfg {
     static constexpr int kWN = 4 / WM, kRowsM = BM / WM, kRowsN = BN / kWN;   // a wavefront's part
     static constexpr int kTM = kRowsM / 32, kTN = kRowsN / 32;                // in blocks of 32 x 32
@@ -145,8 +146,7 @@ struct TileCfg {
     static constexpr int kScaleLoads = (kScaleRows + 3) / 4;
     static constexpr int kLoads = kScaleLoads + kCodeLoads;
     static constexpr int kCodes = (BM + BN) * kGroupBytes, kStage = kCodes + (BM + BN) * 8, kLds = S * kStage;
-    // A step has 4 sub-steps of two blocks a row.  During sub-step FA all operands of the step that are still in
-    // LDS are read; behind it the stage is free, and its refill is issued over SP matrix instructions.
+    // A step has 4 sub-steps of two blocks a row.  Its refill is issued over SP matrix instructions.
     static constexpr int kNS = 4, kMfma = kTM * kTN;
     static constexpr int slot(int i) { return i * SP / kLoads; }
     static constexpr int issued(int slots) {   // loads of a refill issued before the slot
@@ -181,9 +181,9 @@ __device__ __forceinline__ Gemm4Args args_again() {
 
 // WALK: a workgroup has every gridDim-th tile, one behind the other, and the loads of the next tile's first stages are
 // under way while the last ones are multiplied and the output is formed.  Otherwise it has one.
-template <int BM, int BN, int WM, int S, int SP, int FA, int OUT, bool GROUPED, bool WALK>
+template <int BM, int BN, int WM, int S, int SP, int OUT, bool GROUPED, bool WALK>
 __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int tiles_n, int splits) {
-    using C = TileCfg<BM, BN, WM, S, SP, FA>;
+    using C = TileCfg<BM, BN, WM, S, SP>;
     constexpr int TM = C::kTM, TN = C::kTN, NS = C::kNS;
     // a refill ends before the next one begins; vmcnt counts to 63
     static_assert(SP <= NS * C::kMfma && S * C::kLoads < 64 && S >= 2);
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
         uint32_t lane = threadIdx.x % kWave;
         int of_codes = 0, of_scales = 0;
         asm volatile("" : "+v"(lane));   // what follows from it is formed here, and takes no registers in the loop
-        auto fetch = [&](uint32_t r) { return a.index[at.m0 + ((int)r < at.rows_m ? (int)r : at.rows_m - 1)]; };
+        auto fetch = [&](uint32_t r) { return a.index[at.m0 + ((int)r < at.rows_m ? (int)r : 0)]; };
         if (indexed) {
             of_codes = fetch((lane / 8 * 4 + wave) * 8 + lane % 8);
             of_scales = fetch((lane / 32 * 4 + wave) * 32 + lane % 32);
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     const uint32_t row_x = wm * C::kRowsM * kGroupBytes, row_w = (BM + wn * C::kRowsN) * kGroupBytes;
     const uint32_t scale_x = C::kCodes + (wm * C::kRowsM + lane % 32) * 8 + lane / 32 * 4;
     const uint32_t scale_w = C::kCodes + (BM + wn * C::kRowsN + lane % 32) * 8 + lane / 32 * 4;
-    // WALK: operands of a step in parts, below.  Otherwise the operands of a step are read as a whole while the step
+    // WALK: during a step's first sub-step, the operands of its others; behind it the stage is free.  Otherwise the operands of a step are read as a whole while the step
     // before is multiplied, so that a step has one barrier and waits for nothing that it has just asked for.
     constexpr int SETS = WALK ? 1 : 2;
     i32x4 fx[SETS * NS][TM], fw[SETS * NS][TN];
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     };
 
     // The first S - 1 stages, and of the next one what a step issues before it ends.
-    constexpr int kRefillStart = WALK ? (NS - 1 - FA) * C::kMfma : NS * C::kMfma;   // slots of a refill within its own step
+    constexpr int kRefillStart = WALK ? (NS - 1) * C::kMfma : NS * C::kMfma;   // slots of a refill within its own step
     static_assert(C::issued(kRefillStart) == C::kLoads);   // (the walk's stores are behind whole refills)
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -386,17 +386,16 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
                 auto sub_step = [&](auto ks_, auto first_) {
                     constexpr int ks = ks_;
                     constexpr bool FIRST = first_;
-                    if constexpr (ks == FA + 1) {
+                    if constexpr (ks == 1) {
                         // every wavefront has read this stage: its refill may begin
-                        if constexpr (ks < NS - 1) wait_reads();
-                        else wait_stage_behind<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma), kAllStores>(stored && t == 0);
+                        wait_reads();
                         next_step();
                         buffers();
                         refill = buf;
                     } else if constexpr (ks == NS - 1) {
                         wait_stage_behind<(S - 2) * C::kLoads + C::issued(kRefillStart - C::kMfma), kAllStores>(stored && t == 0);
                     }
-                    constexpr int reads = ks < FA || ks == NS - 1 ? kOps : ks == FA ? (NS - 1 - FA) * kOps : 0;
+                    constexpr int reads = ks == 0 ? (NS - 1) * kOps : ks == NS - 1 ? kOps : 0;
                     static_for<C::kMfma>([&](auto j_) {
                         constexpr int j = j_;
                         static_for<reads>([&](auto i) {
@@ -406,7 +405,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
                                 if constexpr (ks == NS - 1) read_scale(i, next_p);
                             }
                         });
-                        constexpr int slot = ((ks + NS - 1 - FA) % NS) * C::kMfma + j;
+                        constexpr int slot = ((ks + NS - 1) % NS) * C::kMfma + j;
                         static_for<C::kLoads>([&](auto i) {
                             if constexpr (C::slot(i) == slot) load(i, lds0 + refill * C::kStage);
                         });
@@ -584,14 +583,14 @@ __global__ __launch_bounds__(256) void k_gemm4_join(Gemm4Args a, int splits) {
     }
 }
 
-template <int BM, int BN, int WM, int S, int SP, int FA, int OUT, bool GROUPED>
+template <int BM, int BN, int WM, int S, int SP, int OUT, bool GROUPED>
 hipError_t launch_tile_kernel(const Gemm4Args& a, int tiles_m, int tiles_n, int splits, hipStream_t st) {
-    using C = TileCfg<BM, BN, WM, S, SP, FA>;
+    using C = TileCfg<BM, BN, WM, S, SP>;
     // the walk's output goes through LDS of its own (4 KiB a wavefront)
     constexpr int kOut = 16384;
     constexpr bool WALK = BM * BN == 256 * 256;
     constexpr int kLds = C::kLds + (WALK ? kOut : 0);
-    auto kernel = k_gemm4<BM, BN, WM, S, SP, FA, OUT, GROUPED, WALK>;
+    auto kernel = k_gemm4<BM, BN, WM, S, SP, OUT, GROUPED, WALK>;
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_big_lds(kernel, kLds, done);
     if (e != hipSuccess) return e;
@@ -600,29 +599,29 @@ hipError_t launch_tile_kernel(const Gemm4Args& a, int tiles_m, int tiles_n, int 
                          splits);
 }
 
-template <int BM, int BN, int WM, int S, int SP, int FA>
+template <int BM, int BN, int WM, int S, int SP>
 hipError_t launch_tiles(const Gemm4Args& a, hipStream_t st) {
     const int tiles_m = (int)(((int64_t)a.M + BM - 1) / BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
-    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, FA, kBf16, false>(a, tiles_m, tiles_n, 1, st)
-                    : launch_tile_kernel<BM, BN, WM, S, SP, FA, kF32, false>(a, tiles_m, tiles_n, 1, st);
+    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, kBf16, false>(a, tiles_m, tiles_n, 1, st)
+                    : launch_tile_kernel<BM, BN, WM, S, SP, kF32, false>(a, tiles_m, tiles_n, 1, st);
 }
 
 // The same, or with k in parts and their join.
-template <int BM, int BN, int WM, int S, int SP, int FA>
+template <int BM, int BN, int WM, int S, int SP>
 hipError_t launch_tiles_or_parts(const Gemm4Args& a, int splits, hipStream_t st) {
-    if (splits == 1) return launch_tiles<BM, BN, WM, S, SP, FA>(a, st);
+    if (splits == 1) return launch_tiles<BM, BN, WM, S, SP>(a, st);
     const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
-    const hipError_t e = launch_tile_kernel<BM, BN, WM, S, SP, FA, kSums, false>(a, tiles_m, tiles_n, splits, st);
+    const hipError_t e = launch_tile_kernel<BM, BN, WM, S, SP, kSums, false>(a, tiles_m, tiles_n, splits, st);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)(((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256));
     return launch_kernel(a.y_bf16 ? k_gemm4_join<true> : k_gemm4_join<false>, grid, 256, 0, st, a, splits);
 }
 
-template <int BM, int BN, int WM, int S, int SP, int FA>
+template <int BM, int BN, int WM, int S, int SP>
 hipError_t launch_group_tiles(const Gemm4Args& a, hipStream_t st) {
     const int tiles_m = (int)group_tiles(a.M, a.experts, BM), tiles_n = (int)(((int64_t)a.N + BN - 1) / BN);
-    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, FA, kBf16, true>(a, tiles_m, tiles_n, 1, st)
-                    : launch_tile_kernel<BM, BN, WM, S, SP, FA, kF32, true>(a, tiles_m, tiles_n, 1, st);
+    return a.y_bf16 ? launch_tile_kernel<BM, BN, WM, S, SP, kBf16, true>(a, tiles_m, tiles_n, 1, st)
+                    : launch_tile_kernel<BM, BN, WM, S, SP, kF32, true>(a, tiles_m, tiles_n, 1, st);
 }
 
 // Few activation rows: bound by the one read of the weights (1 x 5120 x 5120: 4.6 us, 3.0 TB/s with a launch in it; 1 x
@@ -659,7 +658,7 @@ __global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows,
     const uint8_t* ring_p = lds + wave * S * kUnit;
     const bool indexed = GROUPED && a.index;
     auto x_row = [&](int r, bool& none) {
-        const int row = a.index[m0 + (r < rows_m ? r : rows_m - 1)];
+        const int row = a.index[m0 + (r < rows_m ? r : 0)];
         none = r >= rows_m || row < 0 || row >= a.x_rows;
         return row;
     };
@@ -811,22 +810,22 @@ size_t gemm4_workspace(int M, int N, int groups) {
 hipError_t launch_gemm4(const Gemm4Args& a, hipStream_t st) {
     const Plan4 p = plan4(a.M, a.N, a.groups);
     switch (p.tile) {
-    case 0: return launch_tiles<256, 256, 2, 2, 48, 0>(a, st);
-    case 1: return launch_tiles_or_parts<128, 256, 2, 3, 32, 0>(a, p.splits, st);
-    case 2: return launch_tiles_or_parts<128, 128, 2, 3, 16, 0>(a, p.splits, st);
-    case 3: return launch_tiles_or_parts<64, 256, 1, 3, 16, 0>(a, p.splits, st);
-    case 4: return launch_tiles_or_parts<32, 256, 1, 4, 8, 0>(a, p.splits, st);
-    case 5: return launch_tiles_or_parts<64, 64, 2, 4, 4, 0>(a, p.splits, st);
+    case 0: return launch_tiles<256, 256, 2, 2, 48>(a, st);
+    case 1: return launch_tiles_or_parts<128, 256, 2, 3, 32>(a, p.splits, st);
+    case 2: return launch_tiles_or_parts<128, 128, 2, 3, 16>(a, p.splits, st);
+    case 3: return launch_tiles_or_parts<64, 256, 1, 3, 16>(a, p.splits, st);
+    case 4: return launch_tiles_or_parts<32, 256, 1, 4, 8>(a, p.splits, st);
+    case 5: return launch_tiles_or_parts<64, 64, 2, 4, 4>(a, p.splits, st);
     default: return a.y_bf16 ? launch_thin<kBf16>(a, st) : launch_thin<kF32>(a, st);
     }
 }
 
 hipError_t launch_gemm4_grouped(const Gemm4Args& a, hipStream_t st) {
     switch (plan4_grouped(a.M, a.experts, a.N, a.groups)) {
-    case 0: return launch_group_tiles<256, 256, 2, 2, 48, 0>(a, st);
-    case 1: return launch_group_tiles<128, 256, 2, 3, 32, 0>(a, st);
-    case 3: return launch_group_tiles<64, 256, 1, 3, 16, 0>(a, st);
-    case 4: return launch_group_tiles<32, 256, 1, 4, 8, 0>(a, st);
+    case 0: return launch_group_tiles<256, 256, 2, 2, 48>(a, st);
+    case 1: return launch_group_tiles<128, 256, 2, 3, 32>(a, st);
+    case 3: return launch_group_tiles<64, 256, 1, 3, 16>(a, st);
+    case 4: return launch_group_tiles<32, 256, 1, 4, 8>(a, st);
     case kThin4: return launch_group_thin<1>(a, st);
     default: return launch_group_thin<2>(a, st);
     }
