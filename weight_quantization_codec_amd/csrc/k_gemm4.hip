@@ -125,15 +125,16 @@ enum { kF32 = 0, kBf16 = 1, kSums = 2 };
 // rows' 128 bytes of codes, then their 8 bytes of scales.
 //
 // What bounds it.  256 x 256 of a group are 64 matrix instructions of 32 cycles for each of the 4 SIMDs, 2099 cycles, in
-// which LDS delivers 128 KiB to the operands and takes in 68.  At 8192 x 13824 x 5120 a step takes 2880 cycles (2590 with
-// empty buffers, 3070 without the matrix instructions), at 1.65 to 1.75 GHz: the chip's power is the limit, and what
+// which LDS delivers 128 KiB to the operands and takes in 68.  At 8192 x 13824 x 5120 a step takes 2670 cycles (2590 with
+// empty buffers; 2970 while the output went through the cache), at 1.71 GHz: the chip's power is the limit, and what
 // moves data takes its part of it.  Matrix instructions from registers alone reach 6.75 PFLOP/s on codes of normal
-// values (9.2 on zeros, at 2.3 GHz); here 4.0 to 4.25.  Smaller tiles have fewer matrix cycles for the bytes that LDS
+// values (9.2 on zeros, at 2.3 GHz); here 4.4.  Smaller tiles have fewer matrix cycles for the bytes that LDS
 // moves: a step of 128 x 128 is 525 matrix cycles and 770 of LDS, and takes 870 with empty buffers.
 //   step by step (us, that size): operands as they stand in memory, no LDS 2557; tiles through LDS, one tile a workgroup
 //   289 (of 70000 cycles a tile 8000 until the first stage is there and 7400 for the output); conversions to bf16 in
 //   pairs 281; workgroups that walk over tiles 276 to 290 on cards where the form before takes 281 to 293 (the cycles
-//   fall by 10%, the clock by 6%).
+//   fall by 10%, the clock by 6%); streaming stores of the output, so that the operands that other tiles read stay in the
+//   cache, 261 where the form before takes 273 to 276 (128 x 256 tiles 388 -> 309; 16384 x 4096 x 2048 83 -> 80).
 //   Not kept: the stage's operands read over two or three sub-steps instead of one (+1%, +12%); a refill
 //   over 32 (+2%) or 60 (-1%, but then a walk's stores stand before loads) instructions; all sums of a part read
 //   before the first conversion (+11%: scratch memory).
@@ -491,7 +492,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
             asm volatile("" : "+v"(to));   // formed here: kept for every store of a tile, addresses need scratch memory
 #pragma unroll
             for (int i = 0; i < kStores; ++i, to += kRowsStore * pitch)
-                *reinterpret_cast<Out16*>(to) = Out16{{held[i][0], held[i][1], held[i][2], held[i][3]}};
+                if constexpr (OUT == kSums)   // which the join reads next
+                    *reinterpret_cast<Out16*>(to) = Out16{{held[i][0], held[i][1], held[i][2], held[i][3]}};
+                else   // streaming: the operands that other tiles read stay in the cache
+                    __builtin_nontemporal_store(held[i], reinterpret_cast<Stream16*>(to));
         };
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {

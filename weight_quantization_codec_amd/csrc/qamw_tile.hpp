@@ -25,6 +25,8 @@ struct __attribute__((packed, aligned(2))) Out16 {
     uint32_t w[4];
 };
 
+typedef uint32_t Stream16 __attribute__((ext_vector_type(4), aligned(2)));   // the same, for streaming stores
+
 struct __attribute__((packed, aligned(2))) Out8 {
     uint32_t w[2];
 };
