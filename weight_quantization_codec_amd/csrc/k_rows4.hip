@@ -98,11 +98,23 @@ __device__ __forceinline__ float gated(float x, float g) {
 }
 
 // Gated values in fp32, which is twice as fast: for g >= -80 the exponential, the reciprocal and the products leave
-// x silu(g) (and its product with a channel scale) within (|g| + 9) 2^-23 < 2^-16 of itself.
-constexpr float kGateError = 0x1p-16f, kGateLeast = -80.0f;
-__device__ __forceinline__ float gated_about(float x, float g) {
+// x silu(g) (and its product with a channel scale) within (|g| + 9) 2^-23 < 2^-16 of itself, as long as what is rounded
+// on the way is a normal number (`lost` is set where it is not):
+//   silu(g), |g| 2^-116 or more for g >= -80, and g / 2 next to 0: normal, or down to 2^-127 with an error of 2^-150,
+//   where g is.  A bf16 g that is not has 7 bits or fewer, and half of it is exact.
+//   x silu(g): without a scale, one below the normal numbers has code 0, or is in a zero block, whichever way it is
+//   rounded, and so it is with a scale of up to kScaleLarge (2^-126 kScaleLarge is less than 0.25 in a block whose
+//   largest value is kZeroBlock).  A larger scale makes a code of it (lost_before_scale).
+constexpr float kGateError = 0x1p-16f, kGateLeast = -80.0f, kScaleLarge = 4.0f;
+constexpr int kSubnormal = 0x90, kZero = 0x60;   // classes of v_cmp_class_f32, of both signs
+template <bool BF>
+__device__ __forceinline__ float gated_about(float x, float g, bool& lost) {
     const float e = __builtin_amdgcn_exp2f(g * -1.44269504088896341f);
+    if constexpr (!BF) lost |= __builtin_amdgcn_classf(g, kSubnormal);
     return g * __builtin_amdgcn_rcpf(1.0f + e) * x;
+}
+__device__ __forceinline__ bool lost_before_scale(float about, float x, float g) {   // (a zero of x or g is exact)
+    return __builtin_amdgcn_classf(about, kSubnormal | kZero) & (__builtin_fminf(__builtin_fabsf(x), __builtin_fabsf(g)) > 0.0f);
 }
 
 // codes_of for values that are known to within kGateError: rounding is monotone, so where both ends of every value's
@@ -148,6 +160,7 @@ __global__ __launch_bounds__(256) void k_quant4(Rows4Args a, int tx, int rows_wg
     if (c >= (a.d + kGroupCols - 1) / kGroupCols * kGroupChunks) return;
     const int have = a.d - j;   // columns of the chunk: below 8 in the last one, none behind it
     float f[kChunk];
+    bool large = false;   // gated: a channel scale that makes codes of values below the normal numbers
     if constexpr (SCALE) {
         if (have >= kChunk)
             unpack<false>(*reinterpret_cast<const Float8*>(a.factor + j), f);
@@ -157,6 +170,11 @@ __global__ __launch_bounds__(256) void k_quant4(Rows4Args a, int tx, int rows_wg
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) bad |= i < have && !(f[i] > 0.0f);
         if (bad && blockIdx.y == 0 && a.status) atomicOr(a.status, QAMW_FLAG_BAD_SCALE);
+        if constexpr (GATE) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) large |= !(__builtin_fabsf(f[i]) <= kScaleLarge);
+            large = __any(large);
+        }
     }
     const int64_t first = (int64_t)blockIdx.y * rows_wg, end = first + rows_wg < a.rows ? first + rows_wg : a.rows;
     bool flag = false;
@@ -164,13 +182,21 @@ __global__ __launch_bounds__(256) void k_quant4(Rows4Args a, int tx, int rows_wg
         uint32_t q, s;
         if constexpr (GATE) {
             float about[kChunk], least = g[0];
+            bool lost = false;
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) {
-                about[i] = gated_about(v[i], g[i]);
-                if constexpr (SCALE) about[i] *= f[i];
+                about[i] = gated_about<BF>(v[i], g[i], lost);
                 least = __builtin_fminf(least, g[i]);
             }
-            const bool sure = codes_about(about, q, s) && least >= kGateLeast;
+            if constexpr (SCALE) {
+                if (large) {
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) lost |= lost_before_scale(about[i], v[i], g[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) about[i] *= f[i];
+            }
+            const bool sure = codes_about(about, q, s) && least >= kGateLeast && !lost;
             if (!__any(!sure)) {
                 store_codes(a, row, c, q, s);
                 return;
