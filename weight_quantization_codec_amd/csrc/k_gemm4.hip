@@ -630,23 +630,23 @@ hipError_t launch_group_tiles(const Gemm4Args& a, hipStream_t st) {
 
 // Few activation rows: bound by the one read of the weights (1 x 5120 x 5120: 4.6 us, 3.0 TB/s with a launch in it; 1 x
 // 13824 x 5120: 7.9, 4.8 TB/s; 96 rows in 32 groups, 4096 x 4096: 58, 4.9 TB/s).  A ring of 2 units, 4 wavefronts: with 3
-// units a workgroup fewer fits a compute unit (10% longer in groups), with 8 wavefronts the same (20%).  A workgroup has up to 32 weight rows and W wavefronts
-// that split k between them.  Each wavefront runs on its own: it loads a group of columns of all rows (a unit) at a
-// time into its own ring of S units in LDS (XL loads of 8 activation rows, 4 of weight rows, and their scales), and
-// waits for nothing but its own loads.
+// units a workgroup fewer fits a compute unit (10% longer in groups), with 8 wavefronts the same (20%).  A workgroup has
+// up to 32 weight rows and W wavefronts that split k between them.  Each wavefront runs on its own: it loads a group of
+// columns of all rows (a unit) at a time into its own ring of S units in LDS (XL loads of 8 activation rows, 4 of weight
+// rows, and the scales of 32 rows of either), and waits for nothing but its own loads.
 template <int W, int S, int XL>
 struct ThinCfg {
-    static constexpr int kMT = XL > 4 ? 2 : 1, kXScales = (XL + 3) / 4;   // blocks and scale loads of activation rows
-    static constexpr int kLoads = 5 + XL + kXScales;
-    static constexpr int kAtX = 4096 + 256, kAtXScales = kAtX + XL * 1024, kUnit = kAtXScales + kXScales * 256;
-    static constexpr int kRing = W * S * kUnit, kPart = W * kMT * 4096, kLds = kRing > kPart ? kRing : kPart;
+    static constexpr int kLoads = 6 + XL;
+    static constexpr int kAtX = 4096 + 256, kAtXScales = kAtX + XL * 1024, kUnit = kAtXScales + 256;
+    static constexpr int kRing = W * S * kUnit, kPart = W * 4096, kLds = kRing > kPart ? kRing : kPart;
 };
 
 template <int W, int S, int XL, int OUT, bool GROUPED>
 __global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows, int tiles_m, int tiles_n) {
     using C = ThinCfg<W, S, XL>;
-    constexpr int MT = C::kMT, kLoads = C::kLoads, kUnit = C::kUnit;
-    static_assert(S * kLoads < 64);   // vmcnt counts to 63
+    constexpr int kLoads = C::kLoads, kUnit = C::kUnit;
+    // vmcnt counts to 63; activation rows are one block of 32, or a part of one
+    static_assert(S * kLoads < 64 && XL <= 4);
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     Tile tile{0, a.M, (int)blockIdx.x * rows, 0, 0, 0};
@@ -666,7 +666,7 @@ __global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows,
         none = r >= rows_m || row < 0 || row >= a.x_rows;
         return row;
     };
-    uint32_t voff_w[4], voff_x[XL], voff_we, voff_xe[C::kXScales];   // the layout of a stage of a tile
+    uint32_t voff_w[4], voff_x[XL], voff_we, voff_xe;   // the layout of a stage of a tile
     voff_we = (uint32_t)lane * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -681,12 +681,11 @@ __global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows,
         if (indexed) row = x_row(row, none);
         voff_x[i] = none ? kFar : (uint32_t)row * (uint32_t)a.ld_x + (uint32_t)((lane % 8) ^ (r / 2 % 8)) * 16;
     }
-#pragma unroll
-    for (int i = 0; i < C::kXScales; ++i) {
-        int row = i * 32 + lane / 2;
+    {
+        uint32_t row = (uint32_t)lane / 2;
         bool none = false;
         if (indexed) row = x_row(row, none);
-        voff_xe[i] = none ? kFar : (uint32_t)row * 8 + lane % 2 * 4;
+        voff_xe = none ? kFar : row * 8 + (uint32_t)lane % 2 * 4;
     }
     const int64_t at_m = indexed ? 0 : m0;
     const uint64_t base_x = (uint64_t)(a.xq + at_m * a.ld_x), base_xe = (uint64_t)(a.xe + at_m * 8);
@@ -710,8 +709,7 @@ __global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows,
         load_lds4(rwe, voff_we, to + 4096);
 #pragma unroll
         for (int i = 0; i < XL; ++i) load_lds16(rx, voff_x[i], to + C::kAtX + i * 1024);
-#pragma unroll
-        for (int i = 0; i < C::kXScales; ++i) load_lds4(rxe, voff_xe[i], to + C::kAtXScales + i * 256);
+        load_lds4(rxe, voff_xe, to + C::kAtXScales);
     };
 #pragma unroll
     for (int s = 0; s < S; ++s) load(u0 + s, s);
@@ -726,48 +724,36 @@ __global__ __launch_bounds__(W * kWave) void k_gemm4_thin(Gemm4Args a, int rows,
     }
     const uint32_t at_we = 4096 + lane % 32 * 8 + lane / 32 * 4;
     const uint32_t at_xe = C::kAtXScales + lane % kWrap * 8 + lane / 32 * 4;
-    f32x16 acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = (f32x16)(0.0f);
+    f32x16 acc = (f32x16)(0.0f);
     int slot = 0;
     for (int u = u0; u < u1; ++u) {
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * kLoads) : "memory");
         const uint8_t* p = ring_p + slot * kUnit;
-        i32x4 fw[4], fx[4][MT];
-        int sx[MT];
-        const int sw = *reinterpret_cast<const int*>(p + at_we);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) sx[m] = *reinterpret_cast<const int*>(p + at_xe + m * 256);
+        i32x4 fw[4], fx[4];
+        const int sw = *reinterpret_cast<const int*>(p + at_we), sx = *reinterpret_cast<const int*>(p + at_xe);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             fw[ks] = *reinterpret_cast<const i32x4*>(p + col_w[ks]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                fx[ks][m] = *reinterpret_cast<const i32x4*>(p + C::kAtX + m * 4096 + col_x[ks]);
+            fx[ks] = *reinterpret_cast<const i32x4*>(p + C::kAtX + col_x[ks]);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot is read: refill it
         load(u + S, slot);
-        static_for<4>([&](auto ks) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m] = mfma4<ks>(fw[ks], fx[ks][m], acc[m], sw, sx[m]);
-        });
+        static_for<4>([&](auto ks) { acc = mfma4<ks>(fw[ks], fx[ks], acc, sw, sx); });
         slot = slot + 1 < S ? slot + 1 : 0;
     }
     wait_stage<0>();
     float* part = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) part[((wave * MT + m) * 16 + i) * kWave + lane] = acc[m][i];
+    for (int i = 0; i < 16; ++i) part[(wave * 16 + i) * kWave + lane] = acc[i];
     __syncthreads();
     const int most = rows_m < XL * 8 ? rows_m : XL * 8;
     for (int o = threadIdx.x; o < most * 32; o += W * kWave) {
         const int m = o / 32, n = o % 32;
         if (n >= rows_n) continue;
-        const float* p = part + (m / 32 * 16 + n / 8 * 4 + n % 4) * kWave + n / 4 % 2 * 32 + m % 32;
+        const float* p = part + (n / 8 * 4 + n % 4) * kWave + n / 4 % 2 * 32 + m % 32;
         float y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) y += p[w * MT * 16 * kWave];
+        for (int w = 0; w < W; ++w) y += p[w * 16 * kWave];
         const int64_t at = (int64_t)(m0 + m) * a.ld_y + n0 + n;
         if constexpr (OUT == kBf16)
             reinterpret_cast<uint16_t*>(a.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)y);

@@ -105,7 +105,7 @@ def _scales4(t, name: str, groups: int, rows: int) -> int:
     return ld
 
 
-def _made(x: torch.Tensor, rows: int, d: int, out, scales) -> Tuple[int, int]:
+def _made(rows: int, d: int, out, scales) -> Tuple[int, int]:
     """The pitches of the codes and scales of a call, given or to be made."""
     groups = mx4_groups(d)
     if (out is None) != (scales is None):
@@ -159,7 +159,7 @@ def quant4(x: torch.Tensor, scale: Optional[torch.Tensor] = None, gate: Optional
         _vec(scale, "scale", d)
     if status is not None:
         _vec(status, "status", 1, torch.int32)
-    ld_q, ld_e = _made(x, rows, d, out, scales)
+    ld_q, ld_e = _made(rows, d, out, scales)
     index = _device(x=x, gate=gate, scale=scale, out=out, scales=scales, status=status)
     if out is None:
         out, scales = _make(x, rows, d)
@@ -217,7 +217,7 @@ def rmsnorm4(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
         _vec(weight, "weight", d)
     if status is not None:
         _vec(status, "status", 1, torch.int32)
-    ld_q, ld_e = _made(x, rows, d, out, scales)
+    ld_q, ld_e = _made(rows, d, out, scales)
     index = _device(x=x, residual=residual, sum_out=sum_out, weight=weight, out=out, scales=scales, status=status)
     if residual is not None and sum_out is None:
         sum_out = x.new_empty(rows, d)
