@@ -20,7 +20,8 @@
  *   Scales: block b of a row (columns 32 b .. 32 b + 31) has the byte at d_e + (b / 8) * ld_e + i * 8 + b % 8, and
  *   every code of the block is times 2^(byte - 127); byte 255 makes the block NaN.  d_e is 8-byte aligned, ld_e a
  *   multiple of 8 and at least 8 rows.  (Groups stand outermost: the rows that a product reads together have
- *   their scales together.)
+ *   their scales together.)  Bytes of other origin that stand by rows, one for every 32 columns, are brought into this
+ *   order by zeros up to 8 kt bytes a row and exchanging rows and groups of 8 bytes; their codes need zeros up to 128 kt.
  * qamw_quant4 and qamw_rmsnorm4 write whole groups: codes past d are 0, scale bytes of blocks past d are 0.
  * The products take whole groups: their sums run over all 256 kt columns.
  *
@@ -79,7 +80,9 @@ int qamw_dequant4(const uint8_t* d_q, int32_t rows, int32_t d, int64_t ld_q, con
  *     h_j = fl32(x_ij + r_ij), or x_ij without d_residual
  *     f   = fl32(1 / sqrt(sum_j h_j^2 / d + eps)), in fp64 but for that rounding
  *     a_j = fl32(fl32(h_j w_j) f)
- * then blocks as above.  h is rounded only where it is stored.
+ * then blocks as above.  h is rounded only where it is stored.  The sum's order goes by rows and d: where 1 / sqrt(..) is
+ * within about d 2^-53 of the middle of two fp32 numbers, f may be the one in one call and the other in a call of more
+ * rows, and codes that lie next to a border may differ.  Calls of the same sizes give the same codes.
  *   d_x, d_residual   rows x d values of x_dtype (d_residual may be NULL), ld_x, ld_res >= d.
  *   d_weight          d fp32 factors w_j, or NULL for all ones.
  *   eps               finite, >= 0.  (A row of zeros with eps = 0 has f infinite and a_j NaN: it is flagged.)

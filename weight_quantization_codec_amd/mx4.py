@@ -9,6 +9,11 @@ all errors among them, the way through this file.  Work is queued on the current
 A matrix of rows x d values is a pair of uint8 tensors: codes, rows x mx4_stride(d) (two columns a byte, whole groups
 of 256 columns), and scales, mx4_groups(d) x rows x 8.  Rows first to last of it are codes[first:last] and
 scales[:, first:last].  The products take whole groups: columns behind d are zeros, as quant4 and rmsnorm4 leave them.
+Codes and scale bytes that stand by rows (rows x ceil(d / 2) and rows x ceil(d / 32)) come into this form by
+
+    pad = torch.nn.functional.pad
+    codes = pad(codes, (0, mx4_stride(d) - codes.shape[1]))
+    scales = pad(scales, (0, 8 * mx4_groups(d) - scales.shape[1])).view(rows, -1, 8).transpose(0, 1).contiguous()
 
 Nothing here has a backward: codes, scales, values read back and products carry no gradient, whatever their inputs
 require.
