@@ -44,8 +44,8 @@ size_t qamw_q8_stride(int32_t d);
 /* Quantize the rows of a matrix (weights, activations, or gated activations).  For every row i:
  *     a_j = x_ij                                       without d_gate
  *         = fl32(x_ij silu(g_ij))                      with d_gate, silu(g) = g / (1 + exp(-g)) in fp32
- *                                                      (to within (|g| + 8) 2^-23 of itself; 0 where
- *                                                      exp(-g) exceeds 2^126)
+ *                                                      (to within (|g| + 8) 2^-23 of itself, or 2^-149;
+ *                                                      0 where exp(-g) exceeds 2^126)
  *     a_j = fl32(a_j s_j)                              with d_scale
  * then codes and row scale as above.
  *   d_x, x_dtype, ld_x   rows x d values (QAMW_F32 or QAMW_BF16), ld_x >= d; any alignment of rows.

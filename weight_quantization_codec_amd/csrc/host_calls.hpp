@@ -86,7 +86,7 @@ inline bool watched() {
 
 // An output on the current device, made by at::empty where that is watched, and otherwise as at::empty makes it at the end
 // of its way through the dispatcher; that way takes as long again (quant4 of a row, calls one behind the other: 4.8 us
-// with it, 4.1 without).
+// with it, 4.3 without).
 inline Tensor make(at::IntArrayRef size, at::ScalarType type) {
     if (watched()) return at::empty(size, at::TensorOptions().device(at::kCUDA).dtype(type));
     return at::detail::empty_generic(size, c10::hip::HIPCachingAllocatorMasqueradingAsCUDA::get(),

@@ -134,7 +134,11 @@ enum { kF32 = 0, kBf16 = 1, kSums = 2 };
 //   289 (of 70000 cycles a tile 8000 until the first stage is there and 7400 for the output); conversions to bf16 in
 //   pairs 281; workgroups that walk over tiles 276 to 290 on cards where the form before takes 281 to 293 (the cycles
 //   fall by 10%, the clock by 6%); streaming stores of the output, so that the operands that other tiles read stay in the
-//   cache, 261 where the form before takes 273 to 276 (128 x 256 tiles 388 -> 309; 16384 x 4096 x 2048 83 -> 80).
+//   cache, 261 where the form before takes 273 to 276 (128 x 256 tiles 388 -> 309; 16384 x 4096 x 2048 83 -> 80).  That
+//   is with three sets of operands by turns; with one set, and with what reads the output behind it (quant4, gated), us,
+//   stored ordinarily and streaming: 1024 x 8192 x 4096 30.5 and 30.2, 2048 x 22016 x 4096 130 and 134, 4096 x 27648 x
+//   5120 381 and 358; 8192 rows in 16 groups, 8192 x 2048, 161 and 170: neither is better for all sizes.
+//   Back to back the chip's power holds for 6 of these products only (263), then they take up to 370 and settle at 305.
 //   Not kept: the stage's operands read over two or three sub-steps instead of one (+1%, +12%); a refill
 //   over 32 (+2%) or 60 (-1%, but then a walk's stores stand before loads) instructions; all sums of a part read
 //   before the first conversion (+11%: scratch memory).
@@ -173,7 +177,9 @@ __device__ __forceinline__ void wait_stage_behind(bool stored) {
 }
 
 // A kernel's first argument, read from memory again: what a loop needs only now and then is not kept in scalar
-// registers, which would not suffice (and a spilled one costs a vector instruction each time).
+// registers, which would not suffice (and a spilled one costs a vector instruction each time).  They do not suffice all
+// the same: the walk has 12 (fp32 output) and 22 (bf16) spilled ones, in groups 50 and 59, most of them used where a
+// tile begins or ends.
 __device__ __forceinline__ Gemm4Args args_again() {
     auto p = __builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(p));
@@ -248,7 +254,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     uint32_t size_x, size_w, size_xe, size_we;
     int load_t, load_steps, load_number = number;
     auto load_from = [&](const Gemm4Args& a, const Tile& at) {
-        // (at most 2^15 groups in 16 parts: 32 bits do, and a division of 64 bits takes a thousand cycles)
+        // (at most 2^15 groups in 8 parts: 32 bits do, and a division of 64 bits takes a thousand cycles)
         const int first = (int)((uint32_t)(a.groups * at.split) / (uint32_t)splits);
         load_steps = (int)((uint32_t)(a.groups * (at.split + 1)) / (uint32_t)splits) - first;
         load_t = 0;
@@ -319,8 +325,9 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
     const uint32_t row_x = wm * C::kRowsM * kGroupBytes, row_w = (BM + wn * C::kRowsN) * kGroupBytes;
     const uint32_t scale_x = C::kCodes + (wm * C::kRowsM + lane % 32) * 8 + lane / 32 * 4;
     const uint32_t scale_w = C::kCodes + (BM + wn * C::kRowsN + lane % 32) * 8 + lane / 32 * 4;
-    // WALK: during a step's first sub-step, the operands of its others; behind it the stage is free.  Otherwise the operands of a step are read as a whole while the step
-    // before is multiplied, so that a step has one barrier and waits for nothing that it has just asked for.
+    // WALK: during a step's first sub-step, the operands of its others; behind it the stage is free.  Otherwise the
+    // operands of a step are read as a whole while the step before is multiplied, so that a step has one barrier and
+    // waits for nothing that it has just asked for.
     constexpr int SETS = WALK ? 1 : 2;
     i32x4 fx[SETS * NS][TM], fw[SETS * NS][TN];
     int sx[TM], sw[TN], next_sx[TM], next_sw[TN];
@@ -379,9 +386,9 @@ __global__ __launch_bounds__(256, 1) void k_gemm4(Gemm4Args a, int tiles_m, int 
                 const int next = buf + 1 < S ? buf + 1 : 0;
                 const uint8_t* cur_p = lds + buf * C::kStage;
                 const uint8_t* next_p = lds + next * C::kStage;
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < TN; ++i) sw[i] = next_sw[i];
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < TM; ++i) sx[i] = next_sx[i];
                 // FIRST: the tile's first products, which are not added to anything
                 auto sub_step = [&](auto ks_, auto first_) {

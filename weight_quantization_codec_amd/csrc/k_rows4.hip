@@ -8,15 +8,16 @@
 // rmsnorm4 holds a row in the registers of 1 to 16 wavefronts, for its sum of squares.
 //
 // Bound by HBM.  Measured (bytes of the rows, codes and scales, against 4.7 TB/s of a large copy): weights with channel
-// scale, 13824 x 5120 bf16, 42 us (4.3 TB/s); gated 2048 x 13824 bf16, 31 us (4.2 TB/s; 40 with every value in fp64);
+// scale, 13824 x 5120 bf16, 42 us (4.3 TB/s); gated 2048 x 13824 bf16, 30 us (4.3 TB/s; 40 with every value in fp64);
 // norm with residual, 4096 x 5120 bf16, 28.8 us (4.8 TB/s; 41.5 with 2 chunks a thread and the weights read again for
 // every row); dequant4 of 13824 x 5120 with channel scale 31 us (5.8 TB/s, part of the codes still in cache).  A single
-// row takes 2.4 to 3.4 us, most of it the launch.  A group's 8 scale bytes of a row are a store of their own; rows one
+// row takes 2.0 to 3.4 us, most of it the launch.  A group's 8 scale bytes of a row are a store of their own; rows one
 // behind the other are one workgroup's, so that L2 joins them to lines (37.9 MB written for 37.6 MB of codes and
 // scales).
 //
 // Rounding.  Values are fp32 from the load on, and every rounding is one that include/qamw_mx4.h names; the sum of squares
-// and the norm's factor are fp64 up to the one rounding of the factor, so that codes do not depend on the order of the sum.
+// and the norm's factor are fp64 up to the one rounding of the factor.  The order of the sum, which goes by the number of
+// rows (norm_shape), decides that rounding only where the factor is within about d 2^-53 of the middle of two fp32 numbers.
 
 #include <type_traits>
 

@@ -1,8 +1,8 @@
 // The ordinary calls of the 4-bit operators, without the interpreter between their checks, as w8_host.cpp has those of
 // the 8-bit ones: a function here returns None for every other call, before anything is queued, and mx4.py does it.
 //
-// Calls one behind the other, one row (us, in the interpreter and here): quant4 8.4 and 4.1, dequant4 7.4 and 3.6,
-// rmsnorm4 with a residual 11 and 4.7, gemm4 10 and 4.4.
+// Calls one behind the other, one row (us, in the interpreter and here): quant4 8.4 and 4.3, dequant4 7.4 and 3.7,
+// rmsnorm4 with a residual 11 and 5.0, gemm4 10 and 4.4.
 #include "host_calls.hpp"
 #include "qamw_mx4.h"
 

@@ -24,8 +24,9 @@ struct TileCost4 {
     double start, more_start, step, more_step;
 };
 // Constants fitted to measurements on MI355X of every tile and 1 to 8 parts on 609 sizes (M from 1 to 8192, N from 64 to
-// 13824, K from 256 to 13824; weights in cache and not).  There the choice takes 0.8% longer than the best one on
-// average, over 10% longer for 17 sizes, and 31% at most.
+// 13824, K from 256 to 13824; weights in cache and not), before the tiles' output was stored streaming.  With the kernels as
+// they are now, on 854 other sizes of that range, the choice takes 1.2% longer than the best one on average, over 10% longer
+// for 36 sizes, and 38% at most (profiles/gemm4_choice.txt).
 constexpr TileCost4 kTiles4[] = {{256, 256, 256, 7.84, 0.93, 1.062, 0.437}, {128, 256, 256, 5.67, 0.0, 0.554, 0.309},
                                  {128, 128, 256, 3.09, 0.0, 0.398, 0.124},  {64, 256, 256, 2.61, 0.79, 0.423, 0.160},
                                  {32, 256, 256, 1.88, 0.99, 0.382, 0.054},  {64, 64, 512, 0.99, 0.78, 0.249, 0.194}};
@@ -72,8 +73,10 @@ inline int64_t group_tiles(int rows, int experts, int bm) { return rows / bm + (
 // Rows in groups.  What the groups are is not known here, only how many rows they have on average; tiles are counted
 // for groups of that many, half a tile more for each that fills one.  The same kind of model, with its own constants
 // (a tile's weights come from memory, not from the tile beside it), fitted to 929 sizes (1 to 64 rows a group and
-// more, in 4 to 64 groups of equal to very different sizes).  The choice takes 2.2% longer than the best one on
-// average there, over 10% longer for a tenth of the sizes, and 50% at most.
+// more, in 4 to 64 groups of equal to very different sizes), before the tiles' output was stored streaming.  With the
+// kernels as they are now, on 1707 other sizes, the choice takes 2.6% longer than the best one on average, over 10% longer
+// for 222 of them (of those, 83 take 16 rows at a time where 8 would be better), and 57% at most (256 x 256 tiles where
+// 128 x 256 would be better, as for most of the largest losses).
 struct GroupCost4 {
     int tile, bm, bn;   // tile: index into kTiles4; kThin4 and kThin4 + 1: few rows of each, 8 and 16 at a time
     double start, step, more_step;

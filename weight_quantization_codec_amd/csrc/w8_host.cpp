@@ -8,8 +8,8 @@
 // memory, for room in a queue): other threads run meanwhile.
 //
 // A call on few rows is over sooner on the GPU (2 to 7 us) than the interpreter has checked its arguments, made
-// its outputs and passed it on (one row, calls one behind the other): quant8 7.5 us there and 4.2 here, dequant8 6.8
-// and 4.0, rmsnorm8 with a residual 10 and 4.8, gemm8 8.4 and 4.2.
+// its outputs and passed it on (one row, calls one behind the other): quant8 7.5 us there and 4.4 here, dequant8 6.8
+// and 4.1, rmsnorm8 with a residual 10 and 5.0, gemm8 8.4 and 4.2.
 #include "host_calls.hpp"
 #include "qamw_w8.h"
 
