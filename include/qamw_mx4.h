@@ -99,7 +99,9 @@ int qamw_rmsnorm4(const void* d_x, qamw_dtype x_dtype, int32_t rows, int32_t d, 
  *     y[m][n] = sum_k x^[m][k] w^[n][k]     over 256 `groups` columns
  * on the matrix cores, which add the products of 64 columns (exact each) at a time to an fp32 sum, within 2^-23 of the
  * largest of the sum's and the products' summed magnitudes; the parts of k that a size is split into are added in a
- * fixed order, so results do not depend on timing.  y is rounded to nearest even for QAMW_BF16.  A block with scale byte
+ * fixed order, so results do not depend on timing.  y is rounded to nearest even for QAMW_BF16.  The two scale bytes of a
+ * product count together, so that neither alone leaves the range of fp32; the sums are fp32 numbers: below the normal ones
+ * they are multiples of 2^-149, and one past the range is infinite, or NaN behind another.  A block with scale byte
  * 255 makes its row of x, or its column of y, NaN.
  *   d_xq, ld_x, d_xe, ld_xe    M rows of codes and their scales.
  *   d_wq, ld_w, d_we, ld_we    d_out rows of codes and their scales.
